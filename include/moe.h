@@ -14,6 +14,11 @@
  *   moe_grouped_quantize_mxfp8 / moe_grouped_ffn_fwd_mxfp8  MXFP8 path
  *   moe_dequantize_rows_mxfp8 / moe_dequantize_weights_mxfp8  operands of
  *                         the MXFP8 path's straight-through backward
+ *   moe_add_rmsnorm       residual addition + RMS norm (bf16 / MXFP8 rows) and
+ *                         moe_add_rmsnorm_bwd; moe_permute_rows_mxfp8 takes its
+ *                         8-bit rows to the experts
+ *   moe_decode            the whole layer for up to 64 tokens
+ *                         (moe_decode_mxfp8: on MXFP8 weights)
  *
  * Conventions for every call:
  *   - Pointers named in a call's doc as "device" are device pointers owned by
@@ -608,6 +613,128 @@ MOE_API moe_status_t moe_dequantize_rows_mxfp8(const uint8_t *codes, const uint8
                                                moe_bf16_t *out, void *ws, size_t ws_bytes, moe_stream_t stream);
 MOE_API moe_status_t moe_dequantize_weights_mxfp8(const uint8_t *data, const uint8_t *scales, int E, int K, int N,
                                                   moe_bf16_t *W, moe_stream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* The norm in front of the block                                       */
+/* ------------------------------------------------------------------ */
+
+/* Residual addition and root-mean-square norm of the block's input rows:
+ *   s = x + residual            (fp32)
+ *   rstd = 1 / sqrt(mean(s^2) + eps)
+ *   y = s * rstd * weight       (fp32, from the unrounded s)
+ * Each output is rounded once from fp32.
+ *
+ *   x        device bf16 [T, H]
+ *   residual device bf16 [T, H], or NULL for none (s = x)
+ *   weight   device bf16 [H]
+ *   eps      >= 0
+ *   sum      device bf16 [T, H] out: s, the new residual stream; required with
+ *            residual, not written without (it would be x).  May be the residual
+ *            or x itself (in place): a row is read before it is written.
+ *   y        device bf16 [T, H] out, or NULL
+ *   y_q,y_sf device uint8 [T, H] E4M3 codes and [T, H/32] UE8M0 scale bytes out
+ *            (row-major; the MX rule of the MXFP8 section), or both NULL
+ *   rstd     device fp32 [T] out, or NULL; needed by the backward
+ * At least one of y and y_q / y_sf.  A row of zeros gives y = 0.
+ *
+ * Limits: H % 8 == 0 (H % 32 == 0 with y_q), H <= 32768, T < 2^31; the bf16 tensors
+ * 16-byte and y_q 8-byte aligned.  T = 0 is a no-op.  Errors: MOE_ERR_INVALID_ARG
+ * (null pointer, negative size, eps negative or NaN, one of y_q / y_sf alone, residual
+ * without sum), MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
+MOE_API moe_status_t moe_add_rmsnorm(const moe_bf16_t *x, const moe_bf16_t *residual, const moe_bf16_t *weight,
+                                     float eps, int64_t T, int H, moe_bf16_t *sum, moe_bf16_t *y, uint8_t *y_q,
+                                     uint8_t *y_sf, float *rstd, moe_stream_t stream);
+
+/* Bytes of device workspace that moe_add_rmsnorm_bwd needs (partial weight
+ * gradients; no initialisation).  0 for invalid sizes. */
+MOE_API size_t moe_rmsnorm_bwd_workspace_bytes(int64_t T, int H);
+
+/* Backward of moe_add_rmsnorm, with xhat = s * rstd taken from the stored s:
+ *   dx = rstd * (w dy - xhat * mean(w dy xhat)) + d_sum     (fp32, rounded once)
+ *   dweight = sum over the rows of dy * xhat                (fp32)
+ * dx is the gradient of x and of the residual alike.
+ *
+ *   dy      device bf16 [T, H]: gradient of y
+ *   d_sum   device bf16 [T, H]: gradient that reaches the stored sum from elsewhere,
+ *           or NULL for none
+ *   sum     device bf16 [T, H]: the forward's sum (its x where it had no residual)
+ *   weight  device bf16 [H];  rstd  device fp32 [T] (from the forward)
+ *   dx      device bf16 [T, H] out (may be dy or d_sum itself)
+ *   dweight device fp32 [H] out, or NULL (then ws may be NULL).  The sum's order is
+ *           fixed: the same inputs give the same bits.  T = 0 writes zeros.
+ *   ws      device workspace of moe_rmsnorm_bwd_workspace_bytes(T, H), 16-byte aligned
+ * Limits as moe_add_rmsnorm.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED,
+ * MOE_ERR_WORKSPACE, MOE_ERR_CUDA. */
+MOE_API moe_status_t moe_add_rmsnorm_bwd(const moe_bf16_t *dy, const moe_bf16_t *d_sum, const moe_bf16_t *sum,
+                                         const moe_bf16_t *weight, const float *rstd, int64_t T, int H,
+                                         moe_bf16_t *dx, float *dweight, void *ws, size_t ws_bytes,
+                                         moe_stream_t stream);
+
+/* moe_permute_mxfp8 for rows that are already MXFP8 (moe_add_rmsnorm's y_q / y_sf):
+ *   rows_q  device uint8 [T, H] E4M3 codes; rows_sf device uint8 [T, H/32] scale bytes
+ * The codes are copied and the scale bytes take the tile layout; every other argument,
+ * output and limit as moe_permute_mxfp8 (rows_q and x_q 16-byte, rows_sf and x_sf 4-byte
+ * aligned). */
+MOE_API moe_status_t moe_permute_rows_mxfp8(const uint8_t *rows_q, const uint8_t *rows_sf, const int32_t *topk_idx,
+                                            int64_t T, int H, int E, int k, uint8_t *x_q, uint8_t *x_sf,
+                                            int64_t rows_cap, int32_t *dst_of_route, int32_t *src_of_row,
+                                            int32_t *group_sizes, int32_t *group_offsets, void *ws, size_t ws_bytes,
+                                            moe_stream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* The whole layer for a few tokens                                     */
+/* ------------------------------------------------------------------ */
+
+/* Most tokens of one moe_decode / moe_decode_mxfp8 call. */
+#define MOE_DECODE_MAX_TOKENS 64
+
+/* Bytes of device workspace of moe_decode and moe_decode_mxfp8 for up to T tokens
+ * (0 for invalid sizes), and its initialisation, once, on `stream`.  The header (error
+ * word, wait limit) is moe_workspace_init's: moe_read_device_error and
+ * moe_workspace_set_wait_limit work on it.  After a call that set MOE_DEVERR_TIMEOUT the
+ * workspace must be initialised again. */
+MOE_API size_t moe_decode_workspace_bytes(int64_t T, int H, int F, int E, int k);
+MOE_API moe_status_t moe_decode_workspace_init(void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* An MoE layer from router logits to output for T <= MOE_DECODE_MAX_TOKENS tokens (token
+ * generation), where the call is bound by reading the weights of the experts hit:
+ *   topk_idx, topk_w = moe_route_topk(logits)            (score_fn MOE_SCORE_SOFTMAX)
+ *                      or moe_route_topk_sigmoid(logits, expert_bias, normalize)
+ *   g = clamp(x_t W_gate[e]), u = clamp(x_t W_up[e])     (e = topk_idx[t, j])
+ *   out_t = bf16(sum_j topk_w[t, j] * (silu(g) * u) W_down[e])
+ * with fp32 sums and one rounding at the end.  The order of the sums is fixed for given
+ * sizes and routing: the same inputs give the same bits.
+ *
+ *   x           device bf16 [T, H];  logits device fp32 [T, E]
+ *   expert_bias device fp32 [E] or NULL (sigmoid router only)
+ *   *_lo, *_hi  inclusive bounds of the SwiGLU inputs (-inf, +inf: no clamp)
+ *   W_gate, W_up device bf16 [E, H, F]; W_down device bf16 [E, F, H]
+ *   topk_idx    device int32 [T, k] out; topk_w device fp32 [T, k] out
+ *   out         device bf16 [T, H] out
+ *   ws          device workspace of moe_decode_workspace_bytes bytes, initialised once; one
+ *               call at a time may use it
+ *
+ * Limits: T <= 64, H % 128 == 0, F % 128 == 0, 1 <= E <= 1024, 1 <= k <= min(E, 32);
+ * x, out, the weights and ws 16-byte aligned.  T = 0 is a no-op.
+ * Errors: MOE_ERR_INVALID_ARG (null pointer, negative size, unknown score_fn, an empty
+ * clamp interval or a NaN bound), MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA;
+ * device: MOE_DEVERR_TIMEOUT. */
+MOE_API moe_status_t moe_decode(const moe_bf16_t *x, const float *logits, const float *expert_bias, int score_fn,
+                                int normalize, float gate_lo, float gate_hi, float up_lo, float up_hi,
+                                const moe_bf16_t *W_gate, const moe_bf16_t *W_up, const moe_bf16_t *W_down, int64_t T,
+                                int H, int F, int E, int k, int32_t *topk_idx, float *topk_w, moe_bf16_t *out,
+                                void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* moe_decode on expert weights kept in MXFP8 (moe_quantize_weights_mxfp8; gate and up with
+ * K = H, N = F, down with K = F, N = H): the weights are the values their codes and scales
+ * stand for.  x and h are not rounded to 8 bits: each enters the block-scaled products as
+ * a sum of E4M3 terms. */
+MOE_API moe_status_t moe_decode_mxfp8(const moe_bf16_t *x, const float *logits, const float *expert_bias,
+                                      int score_fn, int normalize, float gate_lo, float gate_hi, float up_lo,
+                                      float up_hi, const uint8_t *Wg_q, const uint8_t *Wg_sf, const uint8_t *Wu_q,
+                                      const uint8_t *Wu_sf, const uint8_t *Wd_q, const uint8_t *Wd_sf, int64_t T,
+                                      int H, int F, int E, int k, int32_t *topk_idx, float *topk_w, moe_bf16_t *out,
+                                      void *ws, size_t ws_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -21,5 +21,9 @@ from ._binding import (  # noqa: F401
 from ._binding import (  # noqa: F401
     SCORE_SIGMOID, SCORE_SOFTMAX, moe_route_topk_bwd, moe_route_topk_sigmoid,
 )
-from .layer import (HostPipeline, MoeBackward, MoeBackwardMX, MoeForward, MoeForwardMX, MxWeights,  # noqa: F401
-                    moe_forward)
+from ._binding import (  # noqa: F401
+    DECODE_MAX_TOKENS, DecodeWorkspace, NormOutput, NormWorkspace, moe_add_rmsnorm, moe_add_rmsnorm_bwd, moe_decode,
+    moe_decode_mxfp8, moe_permute_rows_mxfp8,
+)
+from .layer import (HostPipeline, MoeBackward, MoeBackwardMX, MoeDecode, MoeDecodeMX, MoeForward,  # noqa: F401
+                    MoeForwardMX, MxWeights, moe_forward)

@@ -76,6 +76,17 @@ SIGNATURES = {
     "moe_unpermute_combine_nvfp4": (_st, [_vp, _vp, _vp, _i64, _int, _int, _vp, _vp, _vp]),
     "moe_dequantize_weights_mxfp8": (_st, [_vp, _vp, _int, _int, _int, _vp, _vp]),
     "moe_grouped_fc2_mxfp8": (_st, [_vp] * 5 + [_int, _int, _int, _i64, _vp, _vp, _sz, _vp]),
+    "moe_add_rmsnorm": (_st, [_vp, _vp, _vp, C.c_float, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_rmsnorm_bwd_workspace_bytes": (_sz, [_i64, _int]),
+    "moe_add_rmsnorm_bwd": (_st, [_vp] * 5 + [_i64, _int, _vp, _vp, _vp, _sz, _vp]),
+    "moe_permute_rows_mxfp8": (_st, [_vp, _vp, _vp, _i64, _int, _int, _int, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
+                                     _sz, _vp]),
+    "moe_decode_workspace_bytes": (_sz, [_i64, _int, _int, _int, _int]),
+    "moe_decode_workspace_init": (_st, [_vp, _sz, _vp]),
+    "moe_decode": (_st, [_vp] * 3 + [_int, _int] + [C.c_float] * 4 + [_vp] * 3 + [_i64, _int, _int, _int, _int]
+                   + [_vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_decode_mxfp8": (_st, [_vp] * 3 + [_int, _int] + [C.c_float] * 4 + [_vp] * 6 + [_i64, _int, _int, _int, _int]
+                         + [_vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
 _lib = None
@@ -516,6 +527,16 @@ class PermutationMX:
     group_offsets: torch.Tensor
     rows_cap: int
 
+    @classmethod
+    def empty(cls, T: int, H: int, E: int, k: int, device="cuda") -> "PermutationMX":
+        """Buffers for T tokens (the scales of rows that no route fills stay 0)."""
+        cap = T * k
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(x_q=torch.empty(cap, H, dtype=torch.uint8, device=device),
+                   x_sf=torch.zeros(mx_tile_scale_bytes(cap, E, H), dtype=torch.uint8, device=device),
+                   dst_of_route=torch.empty(T, k, **i32), src_of_row=torch.empty(cap, **i32),
+                   group_sizes=torch.empty(E, **i32), group_offsets=torch.empty(E + 1, **i32), rows_cap=cap)
+
 
 def moe_permute_mxfp8(x: torch.Tensor, topk_idx: torch.Tensor, E: int, ws: Workspace,
                       out: PermutationMX | None = None, stream=None) -> PermutationMX:
@@ -646,3 +667,201 @@ def moe_unpermute_combine_nvfp4(y_perm: torch.Tensor, dst_of_route: torch.Tensor
     _check("moe_unpermute_combine_nvfp4", load_library().moe_unpermute_combine_nvfp4(
         _ptr(y_perm), _ptr(dst_of_route), _ptr(topk_w), T, H, k, _ptr(out_q), _ptr(out_sf), _stream(stream)))
     return out_q, out_sf
+
+
+# ------------------------------------------------------------------ the norm in front of the block
+
+@dataclass
+class NormOutput:
+    sum: torch.Tensor | None    # [T, H] bf16: x + residual (None without a residual)
+    y: torch.Tensor | None      # [T, H] bf16
+    y_q: torch.Tensor | None    # [T, H] uint8 (E4M3)
+    y_sf: torch.Tensor | None   # [T, H/32] uint8 (UE8M0)
+    rstd: torch.Tensor          # [T] fp32
+
+    @classmethod
+    def empty(cls, T: int, H: int, bf16: bool = True, mxfp8: bool = False, residual: bool = True,
+              device="cuda") -> "NormOutput":
+        if not (bf16 or mxfp8):
+            raise ValueError("at least one of bf16 and mxfp8")
+        if mxfp8 and H % 32:
+            raise ValueError("MXFP8 rows need H % 32 == 0")
+
+        def buf(want, *shape, dtype):
+            return torch.empty(*shape, dtype=dtype, device=device) if want else None
+        return cls(sum=buf(residual, T, H, dtype=torch.bfloat16), y=buf(bf16, T, H, dtype=torch.bfloat16),
+                   y_q=buf(mxfp8, T, H, dtype=torch.uint8), y_sf=buf(mxfp8, T, H // 32, dtype=torch.uint8),
+                   rstd=buf(True, T, dtype=torch.float32))
+
+
+def moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
+                    out: NormOutput | None = None, bf16: bool = True, mxfp8: bool = False, stream=None) -> NormOutput:
+    """sum = x + residual, y = sum * rstd * weight in bf16 and / or MXFP8 along H (moe.h).
+    out: buffers of an earlier NormOutput.empty (which also says which outputs are wanted)."""
+    _need(x, "x", torch.bfloat16)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    dev = x.device
+    _need(weight, "weight", torch.bfloat16, (H,), dev)
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, (T, H), dev)
+    if out is None:
+        out = NormOutput.empty(T, H, bf16, mxfp8, residual is not None, dev)
+    else:
+        _need(out.rstd, "out.rstd", torch.float32, (T,), dev)
+        if residual is not None:
+            _need(out.sum, "out.sum", torch.bfloat16, (T, H), dev)
+        if out.y is not None:
+            _need(out.y, "out.y", torch.bfloat16, (T, H), dev)
+        if out.y_q is not None:
+            _need(out.y_q, "out.y_q", torch.uint8, (T, H), dev)
+            _need(out.y_sf, "out.y_sf", torch.uint8, (T, H // 32), dev)
+    _check("moe_add_rmsnorm", load_library().moe_add_rmsnorm(
+        _ptr(x), _ptr(residual), _ptr(weight), eps, T, H, _ptr(out.sum) if residual is not None else None,
+        _ptr(out.y), _ptr(out.y_q), _ptr(out.y_sf), _ptr(out.rstd), _stream(stream)))
+    return out
+
+
+class NormWorkspace:
+    """Device workspace of moe_add_rmsnorm_bwd (partial weight gradients) for up to T rows of H."""
+
+    def __init__(self, T: int, H: int, device=None):
+        n = int(load_library().moe_rmsnorm_bwd_workspace_bytes(T, H))
+        if n == 0:
+            raise ValueError(f"invalid sizes T={T} H={H}")
+        self.nbytes = n
+        self.buf = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def moe_add_rmsnorm_bwd(dy: torch.Tensor, sum: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                        d_sum: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                        dweight: torch.Tensor | None = None, ws: NormWorkspace | None = None,
+                        want_dweight: bool = True, stream=None):
+    """Gradient of moe_add_rmsnorm (moe.h): (dx bf16 [T, H] of x and the residual alike,
+    dweight fp32 [H] or None).  sum: the forward's sum (its x where it had no residual)."""
+    _need(dy, "dy", torch.bfloat16)
+    if dy.dim() != 2:
+        raise ValueError("dy must be [T, H]")
+    T, H = dy.shape
+    dev = dy.device
+    _need(sum, "sum", torch.bfloat16, (T, H), dev)
+    _need(weight, "weight", torch.bfloat16, (H,), dev)
+    _need(rstd, "rstd", torch.float32, (T,), dev)
+    if d_sum is not None:
+        _need(d_sum, "d_sum", torch.bfloat16, (T, H), dev)
+    if dx is None:
+        dx = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    _need(dx, "dx", torch.bfloat16, (T, H), dev)
+    if dweight is None and want_dweight:
+        dweight = torch.empty(H, dtype=torch.float32, device=dev)
+    if dweight is not None:
+        _need(dweight, "dweight", torch.float32, (H,), dev)
+        if ws is None:
+            ws = NormWorkspace(T, H, dev)
+    _check("moe_add_rmsnorm_bwd", load_library().moe_add_rmsnorm_bwd(
+        _ptr(dy), _ptr(d_sum), _ptr(sum), _ptr(weight), _ptr(rstd), T, H, _ptr(dx), _ptr(dweight),
+        _ptr(ws.buf) if ws is not None else None, ws.nbytes if ws is not None else 0, _stream(stream)))
+    return dx, dweight
+
+
+def moe_permute_rows_mxfp8(rows_q: torch.Tensor, rows_sf: torch.Tensor, topk_idx: torch.Tensor, E: int, ws: Workspace,
+                           out: PermutationMX | None = None, stream=None) -> PermutationMX:
+    """moe_permute_mxfp8 for rows that are already MXFP8: codes uint8 [T, H], row-major
+    scales uint8 [T, H/32] (moe.h)."""
+    _need(rows_q, "rows_q", torch.uint8)
+    if rows_q.dim() != 2:
+        raise ValueError("rows_q must be [T, H]")
+    T, H = rows_q.shape
+    dev = rows_q.device
+    _need(rows_sf, "rows_sf", torch.uint8, (T, H // 32), dev)
+    _need(topk_idx, "topk_idx", torch.int32, None, dev)
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError(f"topk_idx must be [{T}, k]")
+    k = topk_idx.shape[1]
+    if out is None:
+        out = PermutationMX.empty(T, H, E, k, dev)
+    _check("moe_permute_rows_mxfp8", load_library().moe_permute_rows_mxfp8(
+        _ptr(rows_q), _ptr(rows_sf), _ptr(topk_idx), T, H, E, k, _ptr(out.x_q), _ptr(out.x_sf), out.rows_cap,
+        _ptr(out.dst_of_route), _ptr(out.src_of_row), _ptr(out.group_sizes), _ptr(out.group_offsets), _ptr(ws.buf),
+        ws.nbytes, _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------------ the whole layer for a few tokens
+
+DECODE_MAX_TOKENS = 64   # moe.h MOE_DECODE_MAX_TOKENS
+
+
+class DecodeWorkspace(Workspace):
+    """Device workspace of moe_decode / moe_decode_mxfp8 for up to T tokens."""
+
+    def __init__(self, T: int, H: int, F: int, E: int, k: int, device=None, stream=None):
+        n = int(load_library().moe_decode_workspace_bytes(T, H, F, E, k))
+        if n == 0:
+            raise ValueError(f"invalid sizes T={T} H={H} F={F} E={E} k={k}")
+        self.nbytes = n
+        self.buf = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+        self.reset(stream)
+
+    def reset(self, stream=None):
+        _check("moe_decode_workspace_init", load_library().moe_decode_workspace_init(
+            _ptr(self.buf), self.nbytes, _stream(stream)))
+
+
+def _decode_args(x, logits, expert_bias, score_fn, normalize, clamp, E, k, topk_idx, topk_w, out):
+    _need(x, "x", torch.bfloat16)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    dev = x.device
+    _need(logits, "logits", torch.float32, (T, E), dev)
+    if expert_bias is not None:
+        _need(expert_bias, "expert_bias", torch.float32, (E,), dev)
+    if topk_idx is None:
+        topk_idx = torch.empty(T, k, dtype=torch.int32, device=dev)
+    if topk_w is None:
+        topk_w = torch.empty(T, k, dtype=torch.float32, device=dev)
+    if out is None:
+        out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    _need(topk_idx, "topk_idx", torch.int32, (T, k), dev)
+    _need(topk_w, "topk_w", torch.float32, (T, k), dev)
+    _need(out, "out", torch.bfloat16, (T, H), dev)
+    lo, hi = float("-inf"), float("inf")
+    return T, H, topk_idx, topk_w, out, (_ptr(x), _ptr(logits), _ptr(expert_bias), int(score_fn),
+                                         int(bool(normalize)), *(clamp if clamp is not None else (lo, hi, lo, hi)))
+
+
+def moe_decode(x: torch.Tensor, logits: torch.Tensor, W_gate: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tensor,
+               k: int, ws: DecodeWorkspace, score_fn: int = SCORE_SOFTMAX, expert_bias=None, normalize: bool = True,
+               clamp=None, topk_idx=None, topk_w=None, out=None, stream=None):
+    """An MoE layer from logits to output for up to DECODE_MAX_TOKENS tokens (moe.h): (out
+    bf16 [T, H], topk_idx, topk_w).  clamp = (gate_lo, gate_hi, up_lo, up_hi)."""
+    _need(W_gate, "W_gate", torch.bfloat16)
+    if W_gate.dim() != 3:
+        raise ValueError("W_gate must be [E, H, F]")
+    E, _, F = W_gate.shape
+    T, H, topk_idx, topk_w, out, args = _decode_args(x, logits, expert_bias, score_fn, normalize, clamp, E, k, topk_idx,
+                                                     topk_w, out)
+    for name, w, shape in (("W_gate", W_gate, (E, H, F)), ("W_up", W_up, (E, H, F)), ("W_down", W_down, (E, F, H))):
+        _need(w, name, torch.bfloat16, shape, x.device)
+    _check("moe_decode", load_library().moe_decode(
+        *args, _ptr(W_gate), _ptr(W_up), _ptr(W_down), T, H, F, E, k, _ptr(topk_idx), _ptr(topk_w), _ptr(out),
+        _ptr(ws.buf), ws.nbytes, _stream(stream)))
+    return out, topk_idx, topk_w
+
+
+def moe_decode_mxfp8(x: torch.Tensor, logits: torch.Tensor, Wg_q, Wg_sf, Wu_q, Wu_sf, Wd_q, Wd_sf, F: int, k: int,
+                     ws: DecodeWorkspace, score_fn: int = SCORE_SOFTMAX, expert_bias=None, normalize: bool = True,
+                     clamp=None, topk_idx=None, topk_w=None, out=None, stream=None):
+    """moe_decode on MXFP8 expert weights (moe_quantize_weights_mxfp8's codes and scales; moe.h)."""
+    E = logits.shape[-1]
+    T, H, topk_idx, topk_w, out, args = _decode_args(x, logits, expert_bias, score_fn, normalize, clamp, E, k, topk_idx,
+                                                     topk_w, out)
+    for name, t, n in (("Wg_q", Wg_q, 1), ("Wu_q", Wu_q, 1), ("Wd_q", Wd_q, 1), ("Wg_sf", Wg_sf, 32),
+                       ("Wu_sf", Wu_sf, 32), ("Wd_sf", Wd_sf, 32)):
+        _need(t, name, torch.uint8, (E * H * F // n,), x.device)
+    _check("moe_decode_mxfp8", load_library().moe_decode_mxfp8(
+        *args, _ptr(Wg_q), _ptr(Wg_sf), _ptr(Wu_q), _ptr(Wu_sf), _ptr(Wd_q), _ptr(Wd_sf), T, H, F, E, k,
+        _ptr(topk_idx), _ptr(topk_w), _ptr(out), _ptr(ws.buf), ws.nbytes, _stream(stream)))
+    return out, topk_idx, topk_w

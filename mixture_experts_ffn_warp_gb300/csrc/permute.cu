@@ -1030,3 +1030,98 @@ extern "C" moe_status_t moe_permute_mxfp8(const moe_bf16_t *x, const int32_t *to
         return MOE_ERR_CUDA;
     return MOE_OK;
 }
+
+// ---------------------------------------------------------------------------
+// moe_permute_rows_mxfp8: the same permutation of rows that are already MXFP8 (from
+// moe_add_rmsnorm): the codes are copied and each row's scale bytes move from the row-major
+// layout to the operand tile layout of its group.  Bound by memory: 33/32 H bytes read per
+// token, as many written per route.
+// ---------------------------------------------------------------------------
+
+namespace moe {
+namespace {
+
+// One warp per token; lane j < k holds route j's row.
+__global__ void __launch_bounds__(kScatterWarps * 32)
+permute_rows_mx_kernel(const uint4 *__restrict__ x_q, const uint32_t *__restrict__ x_sf,
+                       const int32_t *__restrict__ topk_idx, int64_t T, int k, int E, int H,
+                       const int32_t *__restrict__ chunk_first, const int32_t *__restrict__ group_offsets,
+                       const int32_t *__restrict__ mtile_start, int32_t *__restrict__ dst_of_route,
+                       int32_t *__restrict__ src_of_row, uint4 *__restrict__ out_q, uint8_t *__restrict__ out_sf,
+                       int64_t rows_cap, uint32_t *err) {
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * kScatterWarps + (threadIdx.x >> 5);
+    if (t >= T) return;
+    int my_dst = -1, my_tile = 0, my_m = 0;
+    if (lane < k) {
+        const int64_t r = t * k + lane;
+        int64_t row = dst_of_route[r];   // the final row (cluster count pass) or the rank in its chunk
+        const int e = topk_idx[r];
+        if (chunk_first) {
+            if (row >= 0) row += chunk_first[(r / kPermChunk) * E + e];
+            if (row >= rows_cap) {
+                raise_device_error(err, MOE_DEVERR_CAPACITY);
+                row = -1;
+            }
+            if (row >= 0) src_of_row[row] = (int32_t)r;
+            dst_of_route[r] = (int32_t)row;
+        }
+        if (row >= 0) {
+            const int i = (int)row - group_offsets[e];
+            my_dst = (int)row;
+            my_tile = mtile_start[e] + i / 128;
+            my_m = i % 128;
+        }
+    }
+    const int kb128 = H / 128, vecs = H / 16;
+    for (int j = 0; j < k; ++j) {
+        const int dst = __shfl_sync(0xFFFFFFFFu, my_dst, j);
+        const int tile = __shfl_sync(0xFFFFFFFFu, my_tile, j), m = __shfl_sync(0xFFFFFFFFu, my_m, j);
+        if (dst < 0) continue;
+        for (int v = lane; v < vecs; v += 32) out_q[(int64_t)dst * vecs + v] = x_q[t * vecs + v];
+        for (int b = lane; b < kb128; b += 32)
+            *reinterpret_cast<uint32_t *>(out_sf + mx::tile_sf_offset(tile, kb128, m, 4 * b)) = x_sf[t * kb128 + b];
+    }
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" moe_status_t moe_permute_rows_mxfp8(const uint8_t *rows_q, const uint8_t *rows_sf, const int32_t *topk_idx,
+                                               int64_t T, int H, int E, int k, uint8_t *x_q, uint8_t *x_sf,
+                                               int64_t rows_cap, int32_t *dst_of_route, int32_t *src_of_row,
+                                               int32_t *group_sizes, int32_t *group_offsets, void *ws,
+                                               size_t ws_bytes, moe_stream_t stream) {
+    MOE_NVTX_RANGE("moe_permute_rows_mxfp8");
+    using namespace moe;
+    if (T < 0 || H < 1 || rows_cap < 0) return MOE_ERR_INVALID_ARG;
+    if (E < 1 || E > 1024 || k < 1 || k > 32 || H % 128 != 0) return MOE_ERR_UNSUPPORTED;
+    if (!group_sizes || !group_offsets) return MOE_ERR_INVALID_ARG;
+    const int64_t R = T * (int64_t)k;
+    if (rows_cap < R) return MOE_ERR_INVALID_ARG;
+    if (rows_cap >= 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
+    if (T > 0 && (!rows_q || !rows_sf || !topk_idx || !x_q || !x_sf || !dst_of_route || !src_of_row))
+        return MOE_ERR_INVALID_ARG;
+    if (!all_aligned16({rows_q, x_q}) || reinterpret_cast<uintptr_t>(rows_sf) % 4 ||
+        reinterpret_cast<uintptr_t>(x_sf) % 4)
+        return MOE_ERR_UNSUPPORTED;
+    const size_t need = moe_workspace_bytes(T, E, k);
+    if (!ws || ws_bytes < need || need == 0) return MOE_ERR_WORKSPACE;
+
+    cudaStream_t s = (cudaStream_t)stream;
+    uint32_t *err = ws_error_word(ws);
+    const int64_t chunks = perm_chunks(R);
+    int32_t *counts = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + kWsHeaderBytes);
+    int32_t *mtile = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + kWsHeaderBytes + ws_counts_bytes(chunks, E));
+    bool final_rows = false;
+    if (count_and_scan(topk_idx, R, E, 1, rows_cap, dst_of_route, src_of_row, counts, group_sizes, group_offsets, mtile,
+                       ws_done_counter(ws), err, s, &final_rows) != MOE_OK)
+        return MOE_ERR_CUDA;
+    if (T == 0) return MOE_OK;
+    launch_k(permute_rows_mx_kernel, dim3((unsigned)((T + kScatterWarps - 1) / kScatterWarps)),
+             dim3(kScatterWarps * 32), 0, s, reinterpret_cast<const uint4 *>(rows_q),
+             reinterpret_cast<const uint32_t *>(rows_sf), topk_idx, T, k, E, H, final_rows ? nullptr : counts,
+             group_offsets, mtile, dst_of_route, src_of_row, reinterpret_cast<uint4 *>(x_q), x_sf, rows_cap, err);
+    return launch_status();
+}

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import torch
 
-from ._binding import (SCORE_SIGMOID, SCORE_SOFTMAX, Permutation, PermutationMX, Workspace, moe_combine_bwd,
+from ._binding import (SCORE_SIGMOID, SCORE_SOFTMAX, DecodeWorkspace, Permutation, PermutationMX, Workspace, moe_combine_bwd,
                        moe_grouped_dgrad_fc1, moe_route_topk_bwd, moe_route_topk_sigmoid,
                        moe_grouped_fc1_swiglu_mxfp8, moe_grouped_fc2_mxfp8, moe_permute_mxfp8,
                        moe_dequantize_rows_mxfp8, moe_dequantize_weights_mxfp8, moe_unpermute_combine_mxfp8,
@@ -18,7 +18,7 @@ from ._binding import (SCORE_SIGMOID, SCORE_SOFTMAX, Permutation, PermutationMX,
                        moe_quantize_weights_mxfp8, mx_tile_scale_bytes,
                        moe_grouped_dgrad_fc2_dswiglu, moe_grouped_fc1_swiglu, moe_grouped_fc2,
                        moe_grouped_wgrad, moe_permute, moe_route_topk, moe_unpermute_combine,
-                       moe_unpermute_sum, rows_capacity)
+                       moe_unpermute_sum, rows_capacity, moe_decode, moe_decode_mxfp8, moe_permute_rows_mxfp8)
 
 
 class MoeForward:
@@ -276,7 +276,12 @@ class MoeForwardMX:
     route = MoeForward.route
 
     def permute(self, x, stream=None):
-        moe_permute_mxfp8(x, self.topk_idx, self.E, self.ws, out=self.perm, stream=stream)
+        """x: bf16 rows (quantised on the way), or the (codes, row-major scales) of rows that
+        are already MXFP8 (moe_add_rmsnorm)."""
+        if isinstance(x, tuple):
+            moe_permute_rows_mxfp8(*x, self.topk_idx, self.E, self.ws, out=self.perm, stream=stream)
+        else:
+            moe_permute_mxfp8(x, self.topk_idx, self.E, self.ws, out=self.perm, stream=stream)
 
     def fc1(self, w: MxWeights, stream=None):
         p = self.perm
@@ -340,6 +345,51 @@ class MoeBackwardMX(MoeBackward):
         self.wgrad(stream)
         self.unpermute_sum(stream)
         return self.dx
+
+
+class MoeDecode:
+    """The layer for a few tokens (token generation): routing, expert FFN and combine for up to
+    T <= DECODE_MAX_TOKENS tokens a call, buffers and workspace allocated once.  router /
+    expert_bias / normalize / swiglu_clamp as for MoeForward.  A call takes any number of
+    tokens up to T and returns out (bf16); topk_idx and topk_w are that call's routing."""
+
+    def __init__(self, T: int, H: int, F: int, E: int, k: int, device="cuda", router: str = "softmax",
+                 expert_bias=None, normalize: bool = True, swiglu_clamp=None):
+        if router not in ("softmax", "sigmoid"):
+            raise ValueError("router must be 'softmax' or 'sigmoid'")
+        self.swiglu_clamp = None if swiglu_clamp is None else tuple(float(v) for v in swiglu_clamp)
+        if self.swiglu_clamp is not None and len(self.swiglu_clamp) != 4:
+            raise ValueError("swiglu_clamp is (gate_lo, gate_hi, up_lo, up_hi)")
+        self.T, self.H, self.F, self.E, self.k = T, H, F, E, k
+        self.router, self.expert_bias, self.normalize = router, expert_bias, normalize
+        dev = torch.device(device)
+        self.device = dev
+        self.ws = DecodeWorkspace(T, H, F, E, k, dev)
+        self._out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+        self._idx = torch.empty(T, k, dtype=torch.int32, device=dev)
+        self._w = torch.empty(T, k, dtype=torch.float32, device=dev)
+        self.out, self.topk_idx, self.topk_w = self._out, self._idx, self._w
+
+    def _args(self, x, stream):
+        t = x.shape[0]
+        if t > self.T:
+            raise ValueError(f"at most {self.T} tokens a call, got {t}")
+        if t != self.out.shape[0]:
+            self.out, self.topk_idx, self.topk_w = self._out[:t], self._idx[:t], self._w[:t]
+        return dict(ws=self.ws, score_fn=SCORE_SIGMOID if self.router == "sigmoid" else SCORE_SOFTMAX,
+                    expert_bias=self.expert_bias, normalize=self.normalize, clamp=self.swiglu_clamp,
+                    topk_idx=self.topk_idx, topk_w=self.topk_w, out=self.out, stream=stream)
+
+    def __call__(self, x, logits, W_gate, W_up, W_down, stream=None):
+        return moe_decode(x, logits, W_gate, W_up, W_down, self.k, **self._args(x, stream))[0]
+
+
+class MoeDecodeMX(MoeDecode):
+    """MoeDecode on MXFP8 expert weights (MxWeights); x and the hidden activations stay unquantised."""
+
+    def __call__(self, x, logits, w: MxWeights, stream=None):
+        return moe_decode_mxfp8(x, logits, w.Wg_q, w.Wg_sf, w.Wu_q, w.Wu_sf, w.Wd_q, w.Wd_sf, self.F, self.k,
+                                **self._args(x, stream))[0]
 
 
 class HostPipeline:
