@@ -11,18 +11,24 @@
 // weight element is used from shared memory by all tokens at once and never passes through
 // registers.
 //
-// Work split.  Phase 1 (gate / up) has a unit for each (expert, 128 features, K chunk), phase
-// 2 (down) one for each (256 output columns, expert, K chunk); a unit is 32 KB (bf16) or 33 KB
-// (MXFP8) of weights.  Each phase's units form one line that is cut into equal contiguous
-// ranges, one per CTA, whatever the sizes and the routing.  Where a cut falls inside a tile
-// the CTAs concerned leave fp32 partial sums in the workspace: in phase 1 the last one to
-// arrive adds them (always in CTA order) and applies SwiGLU, in phase 2 each of them adds a
-// slice of the output tile.  No sum's order depends on timing.
+// Work split.  The gate / up products of an expert are tiles of 128 features, the down
+// product's are tiles of 256 output columns; each tile's K range is cut into equal pieces,
+// and a piece of a tile is a segment of the queue that the CTAs draw from: gate / up of all
+// experts hit, in order, then down of all experts, in the same order.  An expert's down
+// segments come long after its gate / up segments, so the weight stream runs on without a
+// pause between the two products.  Segments leave fp32 partial sums in the workspace (a few KB
+// against 128 KB to 2 MB of weights read).  Four join warps per CTA add an expert's gate / up
+// partial sums, apply SwiGLU and write h once all its segments are in; the output is joined
+// from all down segments at the end, by all CTAs.  Which CTA computes a segment depends on
+// timing, the order of every sum does not.
 //
-// Between the phases h must be complete, but not the weight stream: a producer warp loads
-// weights as long as the ring has room, so that the stages filled ahead cover the time in
-// which the last partial sums are joined.  A second producer warp loads the small operand
-// (x, then h) and is the only one that waits.
+// (With each product's units cut into one contiguous range per CTA instead, the SMs' unequal
+// shares of the memory rate left 8 to 12% between the first and the last CTA of each
+// product: one token of the Mixtral shape took 127 us.)
+//
+// A CTA's roles: a warp that draws segments and loads their weights as long as the ring has
+// room, a warp that loads the small operand (x, then h) and is the only one that waits for
+// another CTA, a warp that issues the MMAs, four that drain the accumulators, four that join.
 //
 // Precision.  On bf16 weights h enters phase 2 as two bf16 terms hi + lo in separate columns
 // (N is padded to 16 anyway), so no rounding below fp32 precedes the output's.  On MXFP8
@@ -40,25 +46,46 @@
 namespace moe {
 namespace {
 
-constexpr int kDecThreads = 256;     // warps: weights, x / h, MMA, idle, 4 epilogue
+constexpr int kDecWarps = 12;        // weights, x / h, MMA, idle, 4 drain, 4 join
+constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kDecMaxStages = 8;
 constexpr int kDecMaxCtas = 160;
 constexpr int kDecMaxExperts = 1024;
 constexpr int kABytes = 16384;       // one weight block: 128 output columns x 64 (bf16) / 128 (MXFP8) of K
 constexpr int kSfBytes = 512;        // scale atom of 128 rows x 128 of K
+constexpr int kSegSlots = 4;
 constexpr uint32_t kDecSmemMax = 232448;
 
-// Workspace: header, counters, then data.  The counters are zero between calls.
-constexpr size_t kDecCtrBytes = 4096;
-struct Counters {
-    uint32_t exited;                 // CTAs that have finished
-    uint32_t tiles_done;             // phase 1 tiles whose h is written
+// Workspace: header, counters, then data.  A call uses counter set epoch % 2, which is zero,
+// and zeroes the other one for the next call.
+struct CounterSet {
+    uint32_t queue;                  // segments drawn beyond each CTA's first
     uint32_t x_ready;                // CTAs whose share of x is quantised (MXFP8)
-    uint32_t pad;
-    uint32_t split1[kDecMaxCtas];    // arrivals at the tile that continues past CTA i's range
-    uint32_t split2[kDecMaxCtas];
+    uint32_t finished;               // CTAs whose roles have ended
+    uint32_t down_done;              // down segments whose partial sums are written
+    uint32_t up_done[kDecMaxExperts];   // gate / up segments of the i-th expert hit
+    uint32_t h_done[kDecMaxExperts];    // (token, 128 features) items of its h
 };
-static_assert(sizeof(Counters) <= kDecCtrBytes, "counters");
+struct Counters {
+    uint32_t epoch, pad[3];
+    CounterSet set[2];
+};
+constexpr size_t kDecCtrBytes = (sizeof(Counters) + 1023) / 1024 * 1024;
+
+// Pieces that the K range of a tile is cut into (a rule on the sizes and the number of experts
+// hit, so that it is the same wherever the call runs): about 8 segments per CTA, and finer
+// ones for the down product of the last expert, whose end is the call's end.  More tokens
+// make a segment's partial sums larger: the shortest piece grows with them.  
+struct Pieces {
+    int up, down, last;
+};
+__host__ __device__ inline Pieces pieces_of(int A, int FT, int NT, int K1, int K2, int T) {
+    const int64_t per_cta = (int64_t)A * ((int64_t)FT * K1 + (int64_t)NT * K2) / kDecMaxCtas;
+    const int lo = 1 + T / 16;
+    const int64_t c = per_cta / 8, f = per_cta / 32;
+    const int p = (int)(c < lo ? lo : c > 64 ? 64 : c), l = (int)(f < lo ? lo : f > 8 ? 8 : f);
+    return Pieces{(K1 + p - 1) / p, (K2 + p - 1) / p, (K2 + l - 1) / l};
+}
 
 struct DecArgs {
     const __nv_bfloat16 *x;
@@ -74,10 +101,11 @@ struct DecArgs {
     Counters *ctr;
     uint8_t *xq;                     // MXFP8: x as blocks of the MMA operand
     uint8_t *hq;                     // h as blocks of the MMA operand
-    float *part;                     // partial sums, [CTA][2][T16 * 256]
+    float *part1;                    // partial sums [route][F / 128][piece][256]: gate, up
+    float *part2;                    // partial sums [route][H / 256][piece][256]
     int stages;
     uint32_t stage_bytes;
-    uint32_t off_acc, off_meta;      // shared memory behind the ring
+    uint32_t off_meta;               // shared memory behind the ring
     int nbuf;                        // accumulator buffers in TMEM
 };
 
@@ -132,18 +160,25 @@ __device__ __forceinline__ bool wait_count(const uint32_t *p, uint32_t want, vol
     }
 }
 
-// Barrier of the four epilogue warps; true when `ok` holds in every thread.
-__device__ __forceinline__ bool epi_all(bool ok) {
+// Barrier `ID` of four warps; true when `ok` holds in every thread.
+template <int ID>
+__device__ __forceinline__ bool all_of_four(bool ok) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+        "barrier.cta.red.and.pred q, %2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)ok)
+        : "r"((uint32_t)ok), "n"(ID)
         : "memory");
     return r != 0;
+}
+
+// Counts n events: what this thread wrote, or saw written behind a barrier, is visible to
+// whoever acquires the count.
+__device__ __forceinline__ void count_release(uint32_t *p, uint32_t n) {
+    asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t &r) {
@@ -160,11 +195,6 @@ __device__ __forceinline__ uint32_t order_key(float v) {   // larger ranks first
     const uint32_t b = __float_as_uint(v == 0.0f ? 0.0f : v);
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
-
-// Contiguous range i of n equal shares of U units (every share non-empty when n <= U).
-__device__ __forceinline__ int64_t share_begin(int64_t U, int i, int n) { return U * i / n; }
-// The share that unit u falls in.
-__device__ __forceinline__ int share_of(int64_t u, int64_t U, int n) { return (int)(((u + 1) * n - 1) / U); }
 
 // E4M3 code of v / 2^X and the remainder v - code * 2^X; what is not finite becomes a NaN code.
 __device__ __forceinline__ uint8_t e4m3_term(float v, int X, float &rem) {
@@ -204,20 +234,87 @@ __device__ __forceinline__ float swiglu(float g, float u, const DecArgs &a) {
 
 // ---------------------------------------------------------------- the kernel
 
-// Units of this CTA in one phase, cut at tile ends: next() gives (tile, first chunk, chunks).
-struct Segments {
-    int64_t u, end;
-    int per;   // chunks per tile
-    __device__ bool next(int64_t &tile, int &k0, int &n) {
-        if (u >= end) return false;
-        tile = u / per;
-        k0 = (int)(u - tile * per);
-        const int64_t left = end - u;
-        n = left < per - k0 ? (int)left : per - k0;
-        u += n;
-        return true;
-    }
+// A segment of the queue as the roles of a CTA see it.
+struct Seg {
+    int down;          // 0: gate / up, 1: down, -1: the queue is empty
+    int ai, e;         // which of the experts hit, and its id
+    int tile, piece;   // 128 features / 256 output columns; piece of the tile's K range
+    int k0, n;         // first K chunk, chunks
+    int cnt, c16;      // tokens of the expert, rounded up to 16
+    int r0;            // routes of the experts before it
 };
+
+// Top-k routing of tokens warp, warp + kDecWarps, ... into shared memory: each lane holds experts
+// lane, lane + 32, ... (V of them) in registers.  `meanwhile` runs while the first token's
+// logits are on their way.
+template <int V, typename F>
+__device__ __forceinline__ void route_tokens(const DecArgs &a, int warp, int lane, bool write, uint64_t *s_mask,
+                                             uint16_t *s_idx, float *s_w, F &&meanwhile) {
+    float v[V], bias[V];
+    auto load = [&](int t, float (&to)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) to[i] = lane + 32 * i < a.E ? __ldg(a.logits + (int64_t)t * a.E + lane + 32 * i) : 0.0f;
+    };
+    if (warp < a.T) load(warp, v);
+    if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) bias[i] = a.bias && lane + 32 * i < a.E ? __ldg(a.bias + lane + 32 * i) : 0.0f;
+    }
+    meanwhile();
+    for (int t = warp; t < a.T; t += kDecWarps) {
+        uint32_t key[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float s = v[i];
+            if (a.sigmoid) {
+                s = 1.0f / (1.0f + expf(-s));
+                if (a.bias) s += bias[i];
+            }
+            key[i] = lane + 32 * i < a.E ? order_key(s) : 0u;
+        }
+        if (t + kDecWarps < a.T) load(t + kDecWarps, v);
+        int mine = 0;                                  // lane j keeps the expert of slot j
+        for (int j = 0; j < a.k; ++j) {
+            uint32_t bk = key[0];
+            int bi = 0;
+#pragma unroll
+            for (int i = 1; i < V; ++i)
+                if (key[i] > bk) { bk = key[i]; bi = i; }
+            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, bk);
+            const int e = (int)__reduce_min_sync(0xFFFFFFFFu, bk == top ? (uint32_t)(lane + 32 * bi) : 0xFFFFFFFFu);
+            if (lane == j) mine = e;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (e == lane + 32 * i) key[i] = 0;
+        }
+        const float l = lane < a.k ? __ldg(a.logits + (int64_t)t * a.E + mine) : 0.0f;
+        float w;
+        if (a.sigmoid) {
+            float sc = lane < a.k ? 1.0f / (1.0f + expf(-l)) : 0.0f;
+            if (sc != sc) sc = 0.0f;                   // a NaN logit scores 0
+            float S = sc;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) S += __shfl_xor_sync(0xFFFFFFFFu, S, off);
+            w = a.normalize ? sc / (S + 1e-20f) : sc;
+        } else {
+            const float l0 = __shfl_sync(0xFFFFFFFFu, l, 0);
+            const float ex = (lane < a.k && l0 != -INFINITY) ? expf(l - l0) : 0.0f;
+            float S = ex;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) S += __shfl_xor_sync(0xFFFFFFFFu, S, off);
+            w = l0 == -INFINITY ? 0.0f : ex / S;
+        }
+        if (lane < a.k) {
+            s_idx[t * a.k + lane] = (uint16_t)mine;
+            s_w[t * a.k + lane] = w;
+            atomicOr(reinterpret_cast<unsigned long long *>(&s_mask[mine]), 1ull << t);
+            if (write) {
+                a.topk_idx[t * a.k + lane] = mine;
+                a.topk_w[t * a.k + lane] = w;
+            }
+        }
+    }
+}
 
 template <bool MX>
 __global__ void __launch_bounds__(kDecThreads, 1)
@@ -227,10 +324,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     constexpr uint32_t B_OFF = 2 * kABytes + (MX ? 2 * kSfBytes : 0);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t full_w[kDecMaxStages], full_b[kDecMaxStages], empty[kDecMaxStages], tfull[2], tempty[2], drain;
+    __shared__ uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
+    __shared__ Seg s_seg[kSegSlots];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_active_n;
+    __shared__ int s_active_n, s_joined;
     __shared__ volatile int s_abort;
-    __shared__ uint32_t s_last;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -240,12 +338,16 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     uint64_t *s_mask = reinterpret_cast<uint64_t *>(smem + a.off_meta);   // [E] tokens of each expert, a bit each
     float *s_w = reinterpret_cast<float *>(s_mask + a.E);                 // [T * k]
     int *s_row0 = reinterpret_cast<int *>(s_w + R);                       // [active] padded rows before the expert
-    uint16_t *s_active = reinterpret_cast<uint16_t *>(s_row0 + amax);     // [active] expert ids, ascending
-    uint16_t *s_idx = s_active + amax;                                    // [T * k]
+    int *s_r0 = s_row0 + amax;                                            // [active] routes before the expert
+    uint16_t *s_active = reinterpret_cast<uint16_t *>(s_r0 + amax);       // [active] expert ids, ascending
+    uint16_t *s_idx = s_active + amax;                                    // [T * k] expert of each slot
+    uint16_t *s_route = s_idx + R;                                        // [T * k] its place in expert order
     const uint64_t limit = device_wait_limit(a.err);
     volatile int *abort = &s_abort;
 
-    // ------------------------------------------------------------ set-up
+    // ------------------------------------------------------------ set-up and routing
+    const uint32_t epoch = __ldcg(&a.ctr->epoch);
+    CounterSet *ctr = &a.ctr->set[epoch & 1];
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             sm100::mbar_init(&full_w[s], 1);
@@ -255,6 +357,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
         for (int i = 0; i < 2; ++i) {
             sm100::mbar_init(&tfull[i], 1);
             sm100::mbar_init(&tempty[i], 128);
+        }
+        for (int i = 0; i < kSegSlots; ++i) {
+            sm100::mbar_init(&seg_full[i], 1);
+            sm100::mbar_init(&seg_empty[i], 6);        // x / h, MMA, four drain warps
         }
         sm100::mbar_init(&drain, 1);
         s_abort = 0;
@@ -266,97 +372,46 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     }
     for (int e = threadIdx.x; e < a.E; e += kDecThreads) s_mask[e] = 0;
 
-    if constexpr (MX) {
-        // this CTA's share of x: blocks of 32 elements, a warp each, into [H / 128] blocks of
-        // 2 T16 operand rows (first terms, then second) and a scale atom
-        const int nb = a.H / 32;
-        const uint32_t blk_bytes = (uint32_t)a.T16 * 256 + kSfBytes;
-        for (int b = cta * 8 + warp; b < a.T * nb; b += G * 8) {
-            const int t = b / nb, kb = b - t * nb;
-            uint8_t code[2], sf[2];
-            two_terms(__bfloat162float(a.x[(int64_t)t * a.H + kb * 32 + lane]), code, sf);
-            uint8_t *blk = a.xq + (size_t)(kb / 4) * blk_bytes;
+    // Every CTA routes for itself.  Meanwhile (MXFP8): this CTA's share of x, blocks of 32
+    // elements, a warp each, into [H / 128] blocks of 2 T16 operand rows (first terms, then
+    // second) and a scale atom.
+    auto meanwhile = [&]() {
+        if constexpr (MX) {
+            const int nb = a.H / 32;
+            const uint32_t blk_bytes = (uint32_t)a.T16 * 256 + kSfBytes;
+            for (int b = cta * kDecWarps + warp; b < a.T * nb; b += G * kDecWarps) {
+                const int t = b / nb, kb = b - t * nb;
+                uint8_t code[2], sf[2];
+                two_terms(__bfloat162float(a.x[(int64_t)t * a.H + kb * 32 + lane]), code, sf);
+                uint8_t *blk = a.xq + (size_t)(kb / 4) * blk_bytes;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t n = t + i * a.T16;
-                blk[sw128(n, (kb & 3) * 32 + lane)] = code[i];
-                if (lane == 0) blk[a.T16 * 256 + sf_byte(n, kb & 3)] = sf[i];
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t n = t + i * a.T16;
+                    blk[sw128(n, (kb & 3) * 32 + lane)] = code[i];
+                    if (lane == 0) blk[a.T16 * 256 + sf_byte(n, kb & 3)] = sf[i];
+                }
             }
+            fence_proxy_async_global();
         }
-        fence_proxy_async_global();
-        __threadfence();
-    }
-    sm100::tc_fence_before();
-    __syncthreads();
-    sm100::tc_fence_after();
-    if (MX && threadIdx.x == 0) atomicAdd(&a.ctr->x_ready, 1u);
-
-    // ------------------------------------------------------------ routing, by every CTA for itself
-    {
-        uint32_t *key = reinterpret_cast<uint32_t *>(smem) + warp * a.E;   // the ring is not in use yet
-        for (int t = warp; t < a.T; t += 8) {
-            const float *row = a.logits + (int64_t)t * a.E;
-            uint32_t bk = 0, be = 0;                       // this lane's best key and its expert
-            for (int e = lane; e < a.E; e += 32) {
-                float v = __ldg(row + e);
-                if (a.sigmoid) {
-                    v = 1.0f / (1.0f + expf(-v));
-                    if (a.bias) v += __ldg(a.bias + e);
-                }
-                const uint32_t kk = order_key(v);
-                key[e] = kk;
-                if (kk > bk) { bk = kk; be = e; }
-            }
-            uint32_t mine = 0;                             // lane j keeps the expert of slot j
-            for (int j = 0; j < a.k; ++j) {
-                const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, bk);
-                const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, bk == top ? be : 0xFFFFFFFFu);
-                if (lane == j) mine = e;
-                if ((e & 31) == (uint32_t)lane) {          // the winner's lane looks again
-                    key[e] = 0;
-                    bk = 0;
-                    for (int i = lane; i < a.E; i += 32)
-                        if (key[i] > bk) { bk = key[i]; be = i; }
-                }
-            }
-            float w = 0.0f;
-            if (a.sigmoid) {
-                float sc = lane < a.k ? 1.0f / (1.0f + expf(-__ldg(row + mine))) : 0.0f;
-                if (sc != sc) sc = 0.0f;                   // a NaN logit scores 0
-                float S = sc;
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) S += __shfl_xor_sync(0xFFFFFFFFu, S, off);
-                w = a.normalize ? sc / (S + 1e-20f) : sc;
-            } else {
-                const float l = lane < a.k ? __ldg(row + mine) : 0.0f;
-                const float l0 = __shfl_sync(0xFFFFFFFFu, l, 0);
-                const float ex = (lane < a.k && l0 != -INFINITY) ? expf(l - l0) : 0.0f;
-                float S = ex;
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) S += __shfl_xor_sync(0xFFFFFFFFu, S, off);
-                w = l0 == -INFINITY ? 0.0f : ex / S;
-            }
-            if (lane < a.k) {
-                s_idx[t * a.k + lane] = (uint16_t)mine;
-                s_w[t * a.k + lane] = w;
-                atomicOr(reinterpret_cast<unsigned long long *>(&s_mask[mine]), 1ull << t);
-                if (cta == 0) {
-                    a.topk_idx[t * a.k + lane] = (int32_t)mine;
-                    a.topk_w[t * a.k + lane] = w;
-                }
-            }
-        }
-    }
+        sm100::tc_fence_before();
+        __syncthreads();
+        sm100::tc_fence_after();
+        if (MX && threadIdx.x == 0) count_release(&ctr->x_ready, 1);
+    };
+    if (a.E <= 64) route_tokens<2>(a, warp, lane, cta == 0, s_mask, s_idx, s_w, meanwhile);
+    else if (a.E <= 256) route_tokens<8>(a, warp, lane, cta == 0, s_mask, s_idx, s_w, meanwhile);
+    else route_tokens<32>(a, warp, lane, cta == 0, s_mask, s_idx, s_w, meanwhile);
     __syncthreads();
     if (warp == 0) {
-        // the experts that are hit, ascending, and the 16-row blocks of h before each
-        int n = 0, rows = 0;
+        // the experts that are hit, ascending, with the routes and the 16-row blocks of h before each
+        int n = 0, rows = 0, routes = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             const int e = e0 + lane;
             const uint64_t m = e < a.E ? s_mask[e] : 0;
             const uint32_t hit = __ballot_sync(0xFFFFFFFFu, m != 0);
             if (!hit) continue;
-            int c = (__popcll(m) + 15) & ~15, incl = c;
+            const int c = __popcll(m), mine = (c << 16) | ((c + 15) & ~15);   // both sums at once: each below 2^16
+            int incl = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
@@ -365,76 +420,102 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
             if (m) {
                 const int i = n + __popc(hit & ((1u << lane) - 1));
                 s_active[i] = (uint16_t)e;
-                s_row0[i] = rows + incl - c;
+                s_row0[i] = rows + ((incl - mine) & 0xFFFF);
+                s_r0[i] = routes + ((incl - mine) >> 16);
             }
+            const int sum = __shfl_sync(0xFFFFFFFFu, incl, 31);
             n += __popc(hit);
-            rows += __shfl_sync(0xFFFFFFFFu, incl, 31);
+            rows += sum & 0xFFFF;
+            routes += sum >> 16;
         }
         if (lane == 0) s_active_n = n;
     }
-    sm100::fence_proxy_async_smem();   // the ring's bytes were written as scratch above
     __syncthreads();
 
     const int A = s_active_n;
     const uint32_t tmem = s_tmem;
     const int FT = a.F / 128, K1 = a.H / KC, K2 = a.F / KC, NT = (a.H + 255) / 256;
-    const int64_t U1 = (int64_t)A * FT * K1, U2 = (int64_t)NT * A * K2;
-    const int G1 = U1 < G ? (int)U1 : G, G2 = U2 < G ? (int)U2 : G;
-    // phase 2 tiles here are (output tile, expert) pairs: nt = tile / A, expert = tile % A
-    const Segments none{0, 0, 1};
-    const Segments ph1 = cta < G1 ? Segments{share_begin(U1, cta, G1), share_begin(U1, cta + 1, G1), K1} : none;
-    const Segments ph2 = cta < G2 ? Segments{share_begin(U2, cta, G2), share_begin(U2, cta + 1, G2), K2} : none;
-    const uint32_t row_bytes = MX ? 2u * a.F : 4u * a.F;   // bytes of h per 16-row-block row, both terms
-    auto rows16 = [&](int ai) { return (__popcll(s_mask[s_active[ai]]) + 15) & ~15; };
-    auto h_block = [&](int ai, int c16, int kc) {          // block kc of the expert's h
+    const Pieces pc = pieces_of(A, FT, NT, K1, K2, a.T);
+    const int S2 = pc.down > pc.last ? pc.down : pc.last;   // pieces that part2 has room for
+    const int n_up = A * FT * pc.up, n_down = (A - 1) * NT * pc.down + NT * pc.last;
+    const uint32_t row_bytes = MX ? 2u * a.F : 4u * a.F;    // bytes of h per padded row, both terms
+    auto h_block = [&](int ai, int c16, int kc) {           // block kc of the expert's h
         const uint32_t bytes = (uint32_t)c16 * 256 + (MX ? kSfBytes : 0);
         return a.hq + (size_t)s_row0[ai] * row_bytes + (MX ? (size_t)ai * FT * kSfBytes : 0) + (size_t)kc * bytes;
     };
 
     if (warp == 0) {
-        // ======================================================== weights
+        // ======================================================== queue and weights
         if (lane == 0) {
             const uint64_t pol = evict_first_policy();
-            int stage = 0, issued = 0;
-            uint32_t phase = 0;
+            int stage = 0, issued = 0, slot = 0;
+            uint32_t phase = 0, seg_phase = 0;
             bool ok = true;
-            int64_t tile;
-            int k0, n;
-            for (int ph = 0; ph < 2 && ok; ++ph) {
-                Segments sg = ph == 0 ? ph1 : ph2;
-                while (ok && sg.next(tile, k0, n)) {
-                    const int ai = ph == 0 ? (int)(tile / FT) : (int)(tile % A);
-                    const int e = s_active[ai];
-                    const int col = ph == 0 ? (int)(tile - (int64_t)ai * FT) : 2 * (int)(tile / A);   // 128-column block
-                    const bool two = ph == 0 || (col + 1) * 128 < a.H;
-                    const uint32_t bytes = (two ? 2u : 1u) * (kABytes + (MX ? kSfBytes : 0));
-                    for (int kc = k0; kc < k0 + n; ++kc) {
-                        if (!sm100::mbar_wait(&empty[stage], phase ^ 1u, abort, a.err, limit)) { ok = false; break; }
-                        const uint32_t sa = smem_base + stage * a.stage_bytes;
-                        uint64_t *fb = &full_w[stage];
-                        sm100::mbar_arrive_expect_tx(fb, bytes);
-                        if constexpr (MX) {
-                            const int nblk = (ph == 0 ? a.F : a.H) / 128, K = ph == 0 ? K1 : K2;
-                            const int64_t blk = ((int64_t)e * K + kc) * nblk + col;
-                            for (int i = 0; i < (two ? 2 : 1); ++i) {
-                                const int w = ph == 0 ? i : 2;
-                                const int64_t b = ph == 0 ? blk : blk + i;
-                                bulk_load_hint(sa + i * kABytes, a.wq[w] + b * kABytes, kABytes, fb, pol);
-                                bulk_load_hint(sa + 2 * kABytes + i * kSfBytes, a.wsf[w] + b * kSfBytes, kSfBytes, fb, pol);
-                            }
-                        } else if (ph == 0) {
-                            const int row = e * a.H + kc * KC;
-                            tma_load_3d_hint(sa, &tmG, fb, 0, row, 2 * col, pol);
-                            tma_load_3d_hint(sa + kABytes, &tmU, fb, 0, row, 2 * col, pol);
-                        } else {
-                            const int row = e * a.F + kc * KC;
-                            tma_load_3d_hint(sa, &tmD, fb, 0, row, 2 * col, pol);
-                            if (two) tma_load_3d_hint(sa + kABytes, &tmD, fb, 0, row, 2 * col + 2, pol);
-                        }
-                        ++issued;
-                        if (++stage == a.stages) { stage = 0; phase ^= 1u; }
-                    }
+            int q = cta;
+            while (ok) {
+                Seg s{};
+                int S, K;
+                if (q < n_up) {
+                    s.ai = q / (FT * pc.up);
+                    const int rem = q - s.ai * FT * pc.up;
+                    s.piece = rem / FT;
+                    s.tile = rem - s.piece * FT;
+                    S = pc.up;
+                    K = K1;
+                } else {
+                    const int d = q - n_up, before = (A - 1) * NT * pc.down;
+                    s.down = d < n_down ? 1 : -1;
+                    s.ai = d < before ? d / (NT * pc.down) : A - 1;
+                    const int rem = d - s.ai * NT * pc.down;
+                    s.piece = rem / NT;
+                    s.tile = rem - s.piece * NT;
+                    S = d < before ? pc.down : pc.last;
+                    K = K2;
                 }
+                if (s.down >= 0) {
+                    s.e = s_active[s.ai];
+                    s.k0 = (int)((int64_t)K * s.piece / S);
+                    s.n = (int)((int64_t)K * (s.piece + 1) / S) - s.k0;
+                    s.cnt = __popcll(s_mask[s.e]);
+                    s.c16 = (s.cnt + 15) & ~15;
+                    s.r0 = s_r0[s.ai];
+                }
+                ok = sm100::mbar_wait(&seg_empty[slot], seg_phase ^ 1u, abort, a.err, limit);
+                if (!ok) break;
+                s_seg[slot] = s;
+                sm100::mbar_arrive(&seg_full[slot]);
+                if (++slot == kSegSlots) { slot = 0; seg_phase ^= 1u; }
+                if (s.down < 0) break;
+                const int next = G + (int)atomicAdd(&ctr->queue, 1u);   // drawn ahead: needed after this segment
+                const bool two = !s.down || (2 * s.tile + 1) * 128 < a.H;
+                const uint32_t bytes = (two ? 2u : 1u) * (kABytes + (MX ? kSfBytes : 0));
+                for (int kc = s.k0; kc < s.k0 + s.n; ++kc) {
+                    if (!sm100::mbar_wait(&empty[stage], phase ^ 1u, abort, a.err, limit)) { ok = false; break; }
+                    const uint32_t sa = smem_base + stage * a.stage_bytes;
+                    uint64_t *fb = &full_w[stage];
+                    sm100::mbar_arrive_expect_tx(fb, bytes);
+                    if constexpr (MX) {
+                        const int nblk = (s.down ? a.H : a.F) / 128;
+                        const int64_t blk = ((int64_t)s.e * (s.down ? K2 : K1) + kc) * nblk + (s.down ? 2 * s.tile : s.tile);
+                        for (int i = 0; i < (two ? 2 : 1); ++i) {
+                            const int w = s.down ? 2 : i;
+                            const int64_t b = s.down ? blk + i : blk;
+                            bulk_load_hint(sa + i * kABytes, a.wq[w] + b * kABytes, kABytes, fb, pol);
+                            bulk_load_hint(sa + 2 * kABytes + i * kSfBytes, a.wsf[w] + b * kSfBytes, kSfBytes, fb, pol);
+                        }
+                    } else if (!s.down) {
+                        const int row = s.e * a.H + kc * KC;
+                        tma_load_3d_hint(sa, &tmG, fb, 0, row, 2 * s.tile, pol);
+                        tma_load_3d_hint(sa + kABytes, &tmU, fb, 0, row, 2 * s.tile, pol);
+                    } else {
+                        const int row = s.e * a.F + kc * KC;
+                        tma_load_3d_hint(sa, &tmD, fb, 0, row, 4 * s.tile, pol);
+                        if (two) tma_load_3d_hint(sa + kABytes, &tmD, fb, 0, row, 4 * s.tile + 2, pol);
+                    }
+                    ++issued;
+                    if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+                }
+                q = next;
             }
             if (!ok) {   // the copies already issued land before the CTA exits
                 for (int i = 0; i < a.stages && i < issued; ++i) {
@@ -447,41 +528,40 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     } else if (warp == 1) {
         // ======================================================== x, then h
         if (lane == 0) {
-            int stage = 0, issued = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            int64_t tile;
-            int k0, n;
-            for (int ph = 0; ph < 2 && ok; ++ph) {
-                Segments sg = ph == 0 ? ph1 : ph2;
-                if (sg.u >= sg.end) continue;
-                if (MX && ph == 0) ok = wait_count(&a.ctr->x_ready, (uint32_t)G, abort, a.err, limit);
-                if (ph == 1) ok = wait_count(&a.ctr->tiles_done, (uint32_t)(A * FT), abort, a.err, limit);
-                fence_proxy_async_global();
-                while (ok && sg.next(tile, k0, n)) {
-                    const int ai = (int)(tile % A);        // phase 2's expert
-                    const int c16 = ph == 0 ? 0 : rows16(ai);
-                    for (int kc = k0; kc < k0 + n; ++kc) {
-                        if (!sm100::mbar_wait(&empty[stage], phase ^ 1u, abort, a.err, limit)) { ok = false; break; }
-                        const uint32_t sb = smem_base + stage * a.stage_bytes + B_OFF;
-                        uint64_t *fb = &full_b[stage];
-                        if (ph == 0) {
-                            if constexpr (MX) {
-                                const uint32_t bytes = (uint32_t)a.T16 * 256 + kSfBytes;
-                                sm100::mbar_arrive_expect_tx(fb, bytes);
-                                sm100::bulk_load(sb, a.xq + (size_t)kc * bytes, bytes, fb);
-                            } else {
-                                sm100::mbar_arrive_expect_tx(fb, (uint32_t)a.T16 * 128);
-                                sm100::tma_load_2d(sb, &tmX, fb, kc * KC, 0);
-                            }
-                        } else {
-                            const uint32_t bytes = (uint32_t)c16 * 256 + (MX ? kSfBytes : 0);
-                            sm100::mbar_arrive_expect_tx(fb, bytes);
-                            sm100::bulk_load(sb, h_block(ai, c16, kc), bytes, fb);
-                        }
-                        ++issued;
-                        if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+            int stage = 0, issued = 0, slot = 0, have = -1;
+            uint32_t phase = 0, seg_phase = 0;
+            bool ok = true, have_x = !MX;
+            while (ok) {
+                ok = sm100::mbar_wait(&seg_full[slot], seg_phase, abort, a.err, limit);
+                if (!ok) break;
+                const Seg s = s_seg[slot];
+                sm100::mbar_arrive(&seg_empty[slot]);
+                if (++slot == kSegSlots) { slot = 0; seg_phase ^= 1u; }
+                if (s.down < 0) break;
+                if (!s.down && !have_x) {
+                    ok = wait_count(&ctr->x_ready, (uint32_t)G, abort, a.err, limit);
+                    fence_proxy_async_global();
+                    have_x = true;
+                }
+                if (s.down && s.ai != have) {
+                    ok = wait_count(&ctr->h_done[s.ai], (uint32_t)(FT * s.cnt), abort, a.err, limit);
+                    fence_proxy_async_global();
+                    have = s.ai;
+                }
+                for (int kc = s.k0; ok && kc < s.k0 + s.n; ++kc) {
+                    if (!sm100::mbar_wait(&empty[stage], phase ^ 1u, abort, a.err, limit)) { ok = false; break; }
+                    const uint32_t sb = smem_base + stage * a.stage_bytes + B_OFF;
+                    uint64_t *fb = &full_b[stage];
+                    if (s.down || MX) {
+                        const uint32_t bytes = (uint32_t)(s.down ? s.c16 : a.T16) * 256 + (MX ? kSfBytes : 0);
+                        sm100::mbar_arrive_expect_tx(fb, bytes);
+                        sm100::bulk_load(sb, s.down ? h_block(s.ai, s.c16, kc) : a.xq + (size_t)kc * bytes, bytes, fb);
+                    } else {
+                        sm100::mbar_arrive_expect_tx(fb, (uint32_t)a.T16 * 128);
+                        sm100::tma_load_2d(sb, &tmX, fb, kc * KC, 0);
                     }
+                    ++issued;
+                    if (++stage == a.stages) { stage = 0; phase ^= 1u; }
                 }
             }
             if (!ok) {
@@ -494,65 +574,67 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
         }
     } else if (warp == 2) {
         // ======================================================== MMA issuer
-        int stage = 0, buf = 0;
-        uint32_t phase = 0, acc_phase = 0;
+        int stage = 0, buf = 0, slot = 0;
+        uint32_t phase = 0, acc_phase = 0, seg_phase = 0;
         bool ok = true, issued_any = false;
-        int64_t tile;
-        int k0, n;
         const uint32_t half = 2u * a.T16;                  // columns between the two accumulators of a buffer
-        for (int ph = 0; ph < 2 && ok; ++ph) {
-            Segments sg = ph == 0 ? ph1 : ph2;
-            while (ok && sg.next(tile, k0, n)) {
-                const int N = ph == 0 ? (MX ? 2 * a.T16 : a.T16) : 2 * rows16((int)(tile % A));
-                const bool two = ph == 0 || (2 * (int)(tile / A) + 1) * 128 < a.H;
-                const uint32_t idesc = MX ? sm100::idesc_mxf8(128, N) : sm100::idesc_bf16(128, N, true, false);
-                const bool got = sm100::mbar_wait(&tempty[buf], acc_phase ^ 1u, abort, a.err, limit);
-                if (__any_sync(0xFFFFFFFFu, !got)) { ok = false; break; }
+        while (ok) {
+            const bool got_seg = sm100::mbar_wait(&seg_full[slot], seg_phase, abort, a.err, limit);
+            if (__any_sync(0xFFFFFFFFu, !got_seg)) { ok = false; break; }
+            const int down = s_seg[slot].down, n = s_seg[slot].n, c16 = s_seg[slot].c16, t2 = s_seg[slot].tile;
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(&seg_empty[slot]);
+            if (++slot == kSegSlots) { slot = 0; seg_phase ^= 1u; }
+            if (down < 0) break;
+            const int N = down ? 2 * c16 : MX ? 2 * a.T16 : a.T16;
+            const bool two = !down || (2 * t2 + 1) * 128 < a.H;
+            const uint32_t idesc = MX ? sm100::idesc_mxf8(128, N) : sm100::idesc_bf16(128, N, true, false);
+            const bool got = sm100::mbar_wait(&tempty[buf], acc_phase ^ 1u, abort, a.err, limit);
+            if (__any_sync(0xFFFFFFFFu, !got)) { ok = false; break; }
+            sm100::tc_fence_after();
+            const uint32_t d0 = tmem + (uint32_t)buf * 2 * half, d1 = d0 + half;
+            for (int i = 0; i < n; ++i) {
+                const bool got_w = sm100::mbar_wait(&full_w[stage], phase, abort, a.err, limit) &&
+                                   sm100::mbar_wait(&full_b[stage], phase, abort, a.err, limit);
+                if (__any_sync(0xFFFFFFFFu, !got_w)) { ok = false; break; }
                 sm100::tc_fence_after();
-                const uint32_t d0 = tmem + (uint32_t)buf * 2 * half, d1 = d0 + half;
-                for (int i = 0; i < n; ++i) {
-                    const bool got_w = sm100::mbar_wait(&full_w[stage], phase, abort, a.err, limit) &&
-                                       sm100::mbar_wait(&full_b[stage], phase, abort, a.err, limit);
-                    if (__any_sync(0xFFFFFFFFu, !got_w)) { ok = false; break; }
-                    sm100::tc_fence_after();
-                    const uint32_t sa = smem_base + stage * a.stage_bytes;
-                    const uint64_t ad = MX ? sm100::sdesc_sw128(sa, 16, 1024) : sm100::sdesc_sw128(sa, 8192, 1024);
-                    const uint64_t bd = sm100::sdesc_sw128(sa + B_OFF, 16, 1024);
-                    constexpr uint64_t A_STEP = MX ? (32 >> 4) : (2048 >> 4);   // a K step of 32 / 16 elements
-                    if (sm100::elect_one()) {
-                        if constexpr (MX) {
-                            const uint32_t tsf = tmem + (uint32_t)a.nbuf * 2 * half + stage * 12;
-                            sm100::tmem_cp_32x128b_x4(tsf, sm100::sdesc_plain(sa + 2 * kABytes));
-                            if (two) sm100::tmem_cp_32x128b_x4(tsf + 4, sm100::sdesc_plain(sa + 2 * kABytes + kSfBytes));
-                            sm100::tmem_cp_32x128b_x4(tsf + 8, sm100::sdesc_plain(sa + B_OFF + N * 128));
+                const uint32_t sa = smem_base + stage * a.stage_bytes;
+                const uint64_t ad = MX ? sm100::sdesc_sw128(sa, 16, 1024) : sm100::sdesc_sw128(sa, 8192, 1024);
+                const uint64_t bd = sm100::sdesc_sw128(sa + B_OFF, 16, 1024);
+                constexpr uint64_t A_STEP = MX ? (32 >> 4) : (2048 >> 4);   // a K step of 32 / 16 elements
+                if (sm100::elect_one()) {
+                    if constexpr (MX) {
+                        const uint32_t tsf = tmem + (uint32_t)a.nbuf * 2 * half + stage * 12;
+                        sm100::tmem_cp_32x128b_x4(tsf, sm100::sdesc_plain(sa + 2 * kABytes));
+                        if (two) sm100::tmem_cp_32x128b_x4(tsf + 4, sm100::sdesc_plain(sa + 2 * kABytes + kSfBytes));
+                        sm100::tmem_cp_32x128b_x4(tsf + 8, sm100::sdesc_plain(sa + B_OFF + N * 128));
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                const uint32_t id = idesc | sm100::idesc_sf_ids(kk, kk);
-                                sm100::mma_mxf8(d0, ad + kk * A_STEP, bd + kk * 2, id, tsf, tsf + 8, (i | kk) != 0);
-                                if (two)
-                                    sm100::mma_mxf8(d1, ad + (kABytes >> 4) + kk * A_STEP, bd + kk * 2, id, tsf + 4,
-                                                    tsf + 8, (i | kk) != 0);
-                            }
-                        } else {
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                sm100::mma_bf16(d0, ad + kk * A_STEP, bd + kk * 2, idesc, (i | kk) != 0);
-                                if (two)
-                                    sm100::mma_bf16(d1, ad + (kABytes >> 4) + kk * A_STEP, bd + kk * 2, idesc,
-                                                    (i | kk) != 0);
-                            }
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint32_t id = idesc | sm100::idesc_sf_ids(kk, kk);
+                            sm100::mma_mxf8(d0, ad + kk * A_STEP, bd + kk * 2, id, tsf, tsf + 8, (i | kk) != 0);
+                            if (two)
+                                sm100::mma_mxf8(d1, ad + (kABytes >> 4) + kk * A_STEP, bd + kk * 2, id, tsf + 4,
+                                                tsf + 8, (i | kk) != 0);
                         }
-                        sm100::mma_commit(&empty[stage]);
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            sm100::mma_bf16(d0, ad + kk * A_STEP, bd + kk * 2, idesc, (i | kk) != 0);
+                            if (two)
+                                sm100::mma_bf16(d1, ad + (kABytes >> 4) + kk * A_STEP, bd + kk * 2, idesc,
+                                                (i | kk) != 0);
+                        }
                     }
-                    issued_any = true;
-                    __syncwarp();
-                    if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+                    sm100::mma_commit(&empty[stage]);
                 }
-                if (!ok) break;
-                if (sm100::elect_one()) sm100::mma_commit(&tfull[buf]);
+                issued_any = true;
                 __syncwarp();
-                if (++buf == a.nbuf) { buf = 0; acc_phase ^= 1u; }
+                if (++stage == a.stages) { stage = 0; phase ^= 1u; }
             }
+            if (!ok) break;
+            if (sm100::elect_one()) sm100::mma_commit(&tfull[buf]);
+            __syncwarp();
+            if (++buf == a.nbuf) { buf = 0; acc_phase ^= 1u; }
         }
         if (!ok && issued_any && sm100::elect_one()) {
             // the MMAs already issued finish before TMEM is released
@@ -561,244 +643,120 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
             sm100::mbar_wait(&drain, 0, &dummy, nullptr, 10000000ull);
         }
         __syncwarp();
-    } else if (warp >= 4) {
-        // ======================================================== epilogue
+    } else if (warp >= 4 && warp < 8) {
+        // ======================================================== drain: accumulators -> partial sums
         const int col = (warp - 4) * 32 + lane;            // TMEM lane: feature or output column of a 128 block
         const uint32_t lane_base = (uint32_t)(warp - 4) << 21;   // lane quarter in bits 16..31
-        const bool lead = threadIdx.x == 128;
         const uint32_t half = 2u * a.T16;
-        const int slot_floats = a.T16 * 256;
-        int buf = 0;
-        uint32_t acc_phase = 0;
-        bool ok = true;
-        int64_t tile;
-        int k0, n;
-
-        // h of token i (of the expert's c16 padded rows), features 128 ft + col
-        auto store_h = [&](int ai, int c16, int ft, int i, float v) {
-            if constexpr (MX) {
-                uint8_t code[2], sf[2];
-                two_terms(v, code, sf);
-                uint8_t *blk = h_block(ai, c16, ft);
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const uint32_t r = i + m * c16;
-                    blk[sw128(r, col)] = code[m];
-                    if (lane == 0) blk[c16 * 256 + sf_byte(r, warp - 4)] = sf[m];
-                }
-            } else {
-                const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-                const float hf = __bfloat162float(hi);
-                const __nv_bfloat16 lo = __float2bfloat16_rn(isinf(hf) ? 0.0f : v - hf);
-                uint8_t *blk = h_block(ai, c16, 2 * ft + col / 64);
-                *reinterpret_cast<__nv_bfloat16 *>(blk + sw128(i, (col % 64) * 2)) = hi;
-                *reinterpret_cast<__nv_bfloat16 *>(blk + sw128(i + c16, (col % 64) * 2)) = lo;
-            }
-        };
-        // the tile's h is written by all four warps: visible to the bulk copies, then counted
-        auto tile_done = [&]() {
-            fence_proxy_async_global();
-            __threadfence();
-            epi_all(true);
-            if (lead) atomicAdd(&a.ctr->tiles_done, 1u);
-        };
-
-        // ---------------- phase 1
-        Segments sg = ph1;
-        while (ok && sg.next(tile, k0, n)) {
-            const int ai = (int)(tile / FT), ft = (int)(tile - (int64_t)ai * FT);
-            const int e = s_active[ai], c16 = rows16(ai);
-            const uint64_t mask = s_mask[e];
-            const int cnt = __popcll(mask);
-            const bool whole = n == K1;
-            const int slot = tile == ph1.u / K1 ? 0 : 1;   // the CTA's first tile, or its last
-            float *part = a.part + ((size_t)cta * 2 + slot) * slot_floats;
-            ok = epi_all(sm100::mbar_wait(&tfull[buf], acc_phase, abort, a.err, limit));
-            if (!ok) break;
+        int buf = 0, slot = 0;
+        uint32_t acc_phase = 0, seg_phase = 0;
+        while (true) {
+            bool got = sm100::mbar_wait(&seg_full[slot], seg_phase, abort, a.err, limit);
+            const int down = got ? s_seg[slot].down : -1;
+            if (down >= 0) got = sm100::mbar_wait(&tfull[buf], acc_phase, abort, a.err, limit);
+            if (!all_of_four<1>(got && down >= 0)) break;
+            const Seg s = s_seg[slot];
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(&seg_empty[slot]);
+            if (++slot == kSegSlots) { slot = 0; seg_phase ^= 1u; }
             sm100::tc_fence_after();
-            const uint32_t dg = tmem + lane_base + (uint32_t)buf * 2 * half, du = dg + half;
-            uint64_t m = mask;
-            for (int i0 = 0; i0 < cnt; i0 += 8) {
-                uint32_t g[8] = {}, u[8] = {}, g2[8] = {}, u2[8] = {};
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (i0 + j < cnt) {
-                        const uint32_t t = __ffsll((long long)m) - 1;
-                        m &= m - 1;
-                        tmem_ld1(dg + t, g[j]);
-                        tmem_ld1(du + t, u[j]);
-                        if constexpr (MX) {
-                            tmem_ld1(dg + a.T16 + t, g2[j]);
-                            tmem_ld1(du + a.T16 + t, u2[j]);
-                        }
-                    }
-                tmem_ld_wait8(g);
-                tmem_ld_wait8(u);
-                if constexpr (MX) {
-                    tmem_ld_wait8(g2);
-                    tmem_ld_wait8(u2);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (i0 + j < cnt) {
-                        float gv = __uint_as_float(g[j]), uv = __uint_as_float(u[j]);
-                        if constexpr (MX) {
-                            gv += __uint_as_float(g2[j]);
-                            uv += __uint_as_float(u2[j]);
-                        }
-                        if (whole) {
-                            store_h(ai, c16, ft, i0 + j, swiglu(gv, uv, a));
-                        } else {
-                            part[(i0 + j) * 256 + col] = gv;
-                            part[(i0 + j) * 256 + 128 + col] = uv;
-                        }
-                    }
-            }
-            sm100::tc_fence_before();
-            sm100::mbar_arrive(&tempty[buf]);
-            if (++buf == a.nbuf) { buf = 0; acc_phase ^= 1u; }
-            if (!whole) {
-                // partial sums of CTAs c0..c1; the last to arrive adds them in that order
-                const int c0 = share_of(tile * K1, U1, G1), c1 = share_of(tile * K1 + K1 - 1, U1, G1);
-                __threadfence();
-                epi_all(true);
-                if (lead) {
-                    const uint32_t old = atomicAdd(&a.ctr->split1[c0], 1u);
-                    s_last = old == (uint32_t)(c1 - c0);
-                    if (s_last) a.ctr->split1[c0] = 0;
-                    __threadfence();
-                }
-                epi_all(true);
-                if (!s_last) continue;
-                __threadfence();
-                for (int i = 0; i < cnt; ++i) {
-                    float gv = 0.0f, uv = 0.0f;
-                    for (int c = c0; c <= c1; ++c) {
-                        const int cs = tile == share_begin(U1, c, G1) / K1 ? 0 : 1;
-                        const float *p = a.part + ((size_t)c * 2 + cs) * slot_floats + i * 256 + col;
-                        gv += __ldcg(p);
-                        uv += __ldcg(p + 128);
-                    }
-                    store_h(ai, c16, ft, i, swiglu(gv, uv, a));
-                }
-            }
-            tile_done();
-        }
-
-        // ---------------- phase 2
-        float *acc = reinterpret_cast<float *>(smem + a.off_acc);   // [T][256]; a thread's two columns are its own
-        sg = ph2;
-        int64_t cur = -1;                                  // output tile that acc belongs to
-        const int64_t per_nt = (int64_t)A * K2;
-        const int64_t first_nt = ph2.u / per_nt;
-        // leaves the output tile `nt`: written out, or left to the others as a partial sum
-        auto flush = [&](int64_t nt) {
-            const int cols = a.H - (int)nt * 256 < 256 ? 128 : 256;
-            const int c0 = share_of(nt * per_nt, U2, G2), c1 = share_of(nt * per_nt + per_nt - 1, U2, G2);
-            if (c0 == c1) {
-                for (int t = 0; t < a.T; ++t) {
-                    __nv_bfloat16 *o = a.out + (int64_t)t * a.H + nt * 256 + col;
-                    o[0] = __float2bfloat16_rn(acc[t * 256 + col]);
-                    if (cols == 256) o[128] = __float2bfloat16_rn(acc[t * 256 + 128 + col]);
-                }
-                return;
-            }
-            float *part = a.part + ((size_t)cta * 2 + (nt == first_nt ? 0 : 1)) * slot_floats;
-            for (int t = 0; t < a.T; ++t) {
-                part[t * 256 + col] = acc[t * 256 + col];
-                if (cols == 256) part[t * 256 + 128 + col] = acc[t * 256 + 128 + col];
-            }
-            __threadfence();
-            epi_all(true);
-            if (lead) atomicAdd(&a.ctr->split2[c0], 1u);
-        };
-        while (ok && sg.next(tile, k0, n)) {
-            const int64_t nt = tile / A;
-            const int ai = (int)(tile - nt * A), e = s_active[ai], c16 = rows16(ai);
-            const bool two = (2 * (int)nt + 1) * 128 < a.H;
-            if (nt != cur) {
-                if (cur >= 0) flush(cur);
-                cur = nt;
-                for (int t = 0; t < a.T; ++t) {
-                    acc[t * 256 + col] = 0.0f;
-                    acc[t * 256 + 128 + col] = 0.0f;
-                }
-            }
-            ok = epi_all(sm100::mbar_wait(&tfull[buf], acc_phase, abort, a.err, limit));
-            if (!ok) break;
-            sm100::tc_fence_after();
+            const bool two = !s.down || (2 * s.tile + 1) * 128 < a.H;
             const uint32_t d0 = tmem + lane_base + (uint32_t)buf * 2 * half, d1 = d0 + half;
-            uint64_t m = s_mask[e];
-            const int cnt = __popcll(m);
-            for (int i0 = 0; i0 < cnt; i0 += 8) {
+            // gate / up: column = token, the second term's columns (MXFP8) T16 further;
+            // down: column = token's index in the expert, the second term's c16 further
+            const uint32_t second = s.down ? s.c16 : a.T16;
+            const bool terms = MX || s.down;
+            float *part = s.down ? a.part2 + (((size_t)s.r0 * NT + s.tile) * S2 + s.piece) * 256 + col
+                                 : a.part1 + (((size_t)s.r0 * FT + s.tile) * pc.up + s.piece) * 256 + col;
+            const size_t step = (size_t)(s.down ? NT * S2 : FT * pc.up) * 256;
+            uint64_t m = s_mask[s.e];
+            for (int i0 = 0; i0 < s.cnt; i0 += 8) {
                 uint32_t y0[8] = {}, y1[8] = {}, z0[8] = {}, z1[8] = {};
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (i0 + j < cnt) {
-                        const uint32_t i = i0 + j;
-                        tmem_ld1(d0 + i, y0[j]);
-                        tmem_ld1(d0 + c16 + i, z0[j]);
-                        if (two) {
-                            tmem_ld1(d1 + i, y1[j]);
-                            tmem_ld1(d1 + c16 + i, z1[j]);
+                    if (i0 + j < s.cnt) {
+                        const uint32_t c = s.down ? i0 + j : __ffsll((long long)m) - 1;
+                        m &= m - 1;
+                        tmem_ld1(d0 + c, y0[j]);
+                        if (two) tmem_ld1(d1 + c, y1[j]);
+                        if (terms) {
+                            tmem_ld1(d0 + second + c, z0[j]);
+                            if (two) tmem_ld1(d1 + second + c, z1[j]);
                         }
                     }
                 tmem_ld_wait8(y0);
-                tmem_ld_wait8(z0);
                 tmem_ld_wait8(y1);
+                tmem_ld_wait8(z0);
                 tmem_ld_wait8(z1);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (i0 + j < cnt) {
-                        const int t = __ffsll((long long)m) - 1;
-                        m &= m - 1;
-                        const uint32_t at = __ballot_sync(
-                            0xFFFFFFFFu, lane < a.k && s_idx[t * a.k + (lane < a.k ? lane : 0)] == e);
-                        const float w = s_w[t * a.k + __ffs(at) - 1];
-                        acc[t * 256 + col] += w * (__uint_as_float(y0[j]) + __uint_as_float(z0[j]));
-                        acc[t * 256 + 128 + col] += w * (__uint_as_float(y1[j]) + __uint_as_float(z1[j]));
+                    if (i0 + j < s.cnt) {
+                        float *p = part + (size_t)(i0 + j) * step;
+                        p[0] = __uint_as_float(y0[j]) + __uint_as_float(z0[j]);
+                        if (two) p[128] = __uint_as_float(y1[j]) + __uint_as_float(z1[j]);
                     }
             }
             sm100::tc_fence_before();
             sm100::mbar_arrive(&tempty[buf]);
             if (++buf == a.nbuf) { buf = 0; acc_phase ^= 1u; }
+            all_of_four<1>(true);
+            if (threadIdx.x == 128) count_release(s.down ? &ctr->down_done : &ctr->up_done[s.ai], 1);
         }
-        if (ok && cur >= 0) {
-            flush(cur);
-            // the CTA's split tiles, its first and its last: each contributor adds a slice of the tile
-            for (int i = 0; i < 2 && ok; ++i) {
-                const int64_t nt = i == 0 ? first_nt : cur;
-                if (i == 1 && cur == first_nt) break;
-                const int c0 = share_of(nt * per_nt, U2, G2), c1 = share_of(nt * per_nt + per_nt - 1, U2, G2);
-                if (c0 == c1) continue;
-                bool got = true;
-                if (lead) got = wait_count(&a.ctr->split2[c0], (uint32_t)(c1 - c0 + 1), abort, a.err, limit);
-                ok = epi_all(got);
-                if (!ok) break;
-                __threadfence();
-                const int quads = a.H - (int)nt * 256 < 256 ? 32 : 64, total = a.T * quads;   // 4 columns each
-                const int nc = c1 - c0 + 1, rank = cta - c0;
-                for (int v = total * rank / nc + col; v < total * (rank + 1) / nc; v += 128) {
-                    const int t = v / quads, q = v - t * quads;
-                    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int c = c0; c <= c1; ++c) {
-                        const int cs = nt == share_begin(U2, c, G2) / per_nt ? 0 : 1;
-                        const float4 p = __ldcg(reinterpret_cast<const float4 *>(
-                            a.part + ((size_t)c * 2 + cs) * slot_floats + t * 256 + q * 4));
-                        s.x += p.x;
-                        s.y += p.y;
-                        s.z += p.z;
-                        s.w += p.w;
+    } else if (warp >= 8) {
+        // ======================================================== join: partial sums -> h
+        const int col = (warp - 8) * 32 + lane;
+        const bool lead = threadIdx.x == 256;
+        if (cta == 0) {   // the next call's counters
+            uint32_t *z = reinterpret_cast<uint32_t *>(&a.ctr->set[(epoch & 1) ^ 1]);
+            for (int i = threadIdx.x - 256; i < (int)(sizeof(CounterSet) / 4); i += 128) z[i] = 0;
+        }
+        for (int ai = 0; ai < A; ++ai) {
+            // items (route, 128 features) of the expert; item id belongs to CTA id % G
+            const int r0 = s_r0[ai], cnt = __popcll(s_mask[s_active[ai]]), c16 = (cnt + 15) & ~15;
+            const int end = (r0 + cnt) * FT;
+            int id = r0 * FT;
+            id += (cta - id % G + G) % G;
+            if (id >= end) continue;
+            bool got = true;
+            if (lead) got = wait_count(&ctr->up_done[ai], (uint32_t)(FT * pc.up), abort, a.err, limit);
+            if (!all_of_four<2>(got)) break;
+            uint32_t done = 0;
+            for (; id < end; id += G, ++done) {
+                const int r = id / FT, ft = id - r * FT, i = r - r0;
+                const float *p = a.part1 + (size_t)id * pc.up * 256 + col;
+                float g = 0.0f, u = 0.0f;
+#pragma unroll 8
+                for (int j = 0; j < pc.up; ++j) {
+                    g += __ldcg(p + j * 256);
+                    u += __ldcg(p + j * 256 + 128);
+                }
+                const float v = swiglu(g, u, a);
+                if constexpr (MX) {
+                    uint8_t code[2], sf[2];
+                    two_terms(v, code, sf);
+                    uint8_t *blk = h_block(ai, c16, ft);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        const uint32_t row = i + m * c16;
+                        blk[sw128(row, col)] = code[m];
+                        if (lane == 0) blk[c16 * 256 + sf_byte(row, warp - 8)] = sf[m];
                     }
-                    __nv_bfloat162 o[2] = {__floats2bfloat162_rn(s.x, s.y), __floats2bfloat162_rn(s.z, s.w)};
-                    *reinterpret_cast<uint2 *>(a.out + (int64_t)t * a.H + nt * 256 + q * 4) =
-                        *reinterpret_cast<const uint2 *>(o);
+                } else {
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+                    const float hf = __bfloat162float(hi);
+                    const __nv_bfloat16 lo = __float2bfloat16_rn(isinf(hf) ? 0.0f : v - hf);
+                    uint8_t *blk = h_block(ai, c16, 2 * ft + col / 64);
+                    *reinterpret_cast<__nv_bfloat16 *>(blk + sw128(i, (col % 64) * 2)) = hi;
+                    *reinterpret_cast<__nv_bfloat16 *>(blk + sw128(i + c16, (col % 64) * 2)) = lo;
                 }
             }
+            fence_proxy_async_global();   // read next by bulk copies
+            all_of_four<2>(true);
+            if (lead) count_release(&ctr->h_done[ai], done);
         }
     }
 
-    // ------------------------------------------------------------ teardown
+    // ------------------------------------------------------------ output
     sm100::tc_fence_before();
     __syncthreads();
     if (warp == 2) {
@@ -806,15 +764,59 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
         sm100::tc_fence_after();
         sm100::tmem_dealloc(tmem, 512);
     }
-    if (threadIdx.x == 0) {
-        __threadfence();
-        if (atomicAdd(&a.ctr->exited, 1u) == (uint32_t)G - 1) {   // nobody waits any more: zero for the next call
-            for (int i = 0; i < G; ++i) a.ctr->split2[i] = 0;
-            a.ctr->tiles_done = 0;
-            a.ctr->x_ready = 0;
-            a.ctr->exited = 0;
-            __threadfence();
+    if (threadIdx.x == 32) count_release(&ctr->finished, 1);
+    if (threadIdx.x == 0)
+        s_joined = !s_abort && wait_count(&ctr->down_done, (uint32_t)n_down, abort, a.err, limit);
+    // where each slot's route lies in expert order
+    for (int i = threadIdx.x; i < R; i += kDecThreads) {
+        const int e = s_idx[i], t = i / a.k;
+        int lo = 0, hi = A - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (s_active[mid] < e) lo = mid + 1; else hi = mid;
         }
+        s_route[i] = (uint16_t)(s_r0[lo] + __popcll(s_mask[e] & ((1ull << t) - 1)));
+    }
+    __syncthreads();
+    if (s_joined) {
+        // a thread group of g lanes adds 4 columns of one token over its experts and their pieces
+        const int quads = a.T * (a.H / 4), threads = G * kDecThreads, last_r0 = s_r0[A - 1];
+        int g = 1;
+        while (g < 32 && quads * g * 2 <= threads) g *= 2;
+        const int sub = lane & (g - 1);
+        const int terms = a.k * S2;
+        for (int v0 = 0; v0 < quads; v0 += threads / g) {
+            const int v = v0 + (cta * kDecThreads + (int)threadIdx.x) / g;
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const int t = v / (a.H / 4), c4 = v - t * (a.H / 4), nt = c4 / 64;
+            if (v < quads) {
+#pragma unroll 4
+                for (int i = sub; i < terms; i += g) {
+                    const int j = i / S2, piece = i - j * S2, r = s_route[t * a.k + j];
+                    if (piece >= (r >= last_r0 ? pc.last : pc.down)) continue;
+                    const float w = s_w[t * a.k + j];
+                    const float4 p = __ldcg(reinterpret_cast<const float4 *>(
+                        a.part2 + (((size_t)r * NT + nt) * S2 + piece) * 256 + (c4 - nt * 64) * 4));
+                    s.x += w * p.x;
+                    s.y += w * p.y;
+                    s.z += w * p.z;
+                    s.w += w * p.w;
+                }
+            }
+            for (int off = g >> 1; off > 0; off >>= 1) {
+                s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, off);
+                s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, off);
+                s.z += __shfl_xor_sync(0xFFFFFFFFu, s.z, off);
+                s.w += __shfl_xor_sync(0xFFFFFFFFu, s.w, off);
+            }
+            if (v < quads && sub == 0) {
+                __nv_bfloat162 o[2] = {__floats2bfloat162_rn(s.x, s.y), __floats2bfloat162_rn(s.z, s.w)};
+                *reinterpret_cast<uint2 *>(a.out + (int64_t)t * a.H + c4 * 4) = *reinterpret_cast<const uint2 *>(o);
+            }
+        }
+        // every CTA has read the epoch and drawn its last segment: the next call may begin a new one
+        if (cta == 0 && threadIdx.x == 0 && wait_count(&ctr->finished, (uint32_t)G, abort, a.err, limit))
+            a.ctr->epoch = epoch + 1;
     }
 }
 
@@ -825,21 +827,32 @@ struct Clamp {
 };
 
 struct DecLayout {
-    size_t xq, hq, part, total;
+    size_t xq, hq, part1, part2, total;
 };
 
 size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 int tokens16(int64_t T) { return (int)((T + 15) / 16 * 16); }
 
+// Data behind the counters, sized for the routing that needs most: at least k experts are hit,
+// and the fewer they are the more pieces there are.
 DecLayout decode_layout(int64_t T, int H, int F, int E, int k) {
     const size_t T16 = (size_t)tokens16(T), R = (size_t)(T * k), act = R < (size_t)E ? R : (size_t)E;
     // rows of h padded to 16 per expert hit, two terms of 2 bytes (bf16); the MXFP8 blocks and atoms need less
     const size_t rows = R + 15 * act < act * T16 ? R + 15 * act : act * T16;
+    const int FT = F / 128, NT = (H + 255) / 256;
     DecLayout l;
     l.xq = kWsHeaderBytes + kDecCtrBytes;
     l.hq = l.xq + round_up((size_t)H / 128 * (T16 * 256 + kSfBytes), 1024);
-    l.part = l.hq + round_up(rows * (size_t)F * 4, 1024);
-    l.total = l.part + (size_t)kDecMaxCtas * 2 * T16 * 256 * sizeof(float);
+    l.part1 = l.hq + round_up(rows * (size_t)F * 4, 1024);
+    size_t n1 = 0, n2 = 0;
+    for (int kc = 64; kc <= 128; kc += 64) {   // K chunks of 64 (bf16) and 128 (MXFP8)
+        const Pieces p = pieces_of(k, FT, NT, H / kc, F / kc, (int)T);
+        const size_t down = p.down > p.last ? p.down : p.last;
+        n1 = (size_t)p.up > n1 ? p.up : n1;
+        n2 = down > n2 ? down : n2;
+    }
+    l.part2 = l.part1 + R * FT * n1 * 1024;
+    l.total = l.part2 + R * NT * n2 * 1024;
     return l;
 }
 
@@ -877,28 +890,26 @@ moe_status_t launch_decode(DecArgs a, const moe_bf16_t *const (&W)[3], void *ws,
     a.ctr = reinterpret_cast<Counters *>(base + kWsHeaderBytes);
     a.xq = reinterpret_cast<uint8_t *>(base + l.xq);
     a.hq = reinterpret_cast<uint8_t *>(base + l.hq);
-    a.part = reinterpret_cast<float *>(base + l.part);
+    a.part1 = reinterpret_cast<float *>(base + l.part1);
+    a.part2 = reinterpret_cast<float *>(base + l.part2);
 
     const int R = a.T * a.k, act = R < a.E ? R : a.E;
     const uint32_t b_bytes = (uint32_t)a.T16 * 256 + (MX ? 3 * kSfBytes : 0);   // x or h, all scale atoms
     a.stage_bytes = (uint32_t)round_up(2 * kABytes + b_bytes, 1024);
-    const uint32_t acc = (uint32_t)a.T16 * 1024;
-    const uint32_t meta = (uint32_t)a.E * 8 + R * 4 + act * 4 + act * 2 + R * 2;
-    const uint32_t fixed = acc + (uint32_t)round_up(meta, 16) + 1024 /* alignment */ + 1024 /* static */;
-    int stages = (int)((kDecSmemMax - fixed) / a.stage_bytes);
+    const uint32_t meta = (uint32_t)round_up(a.E * 8 + R * 4 + act * 8 + act * 2 + R * 4, 16);
+    const uint32_t fixed = meta + 1024 /* alignment */ + 2048 /* static */;
+    const int stages = (int)((kDecSmemMax - fixed) / a.stage_bytes);
     a.stages = stages < kDecMaxStages ? stages : kDecMaxStages;
-    if (a.stages < 2) return MOE_ERR_UNSUPPORTED;
-    a.off_acc = a.stages * a.stage_bytes;
-    a.off_meta = a.off_acc + acc;
+    a.off_meta = a.stages * a.stage_bytes;
     a.nbuf = 8 * a.T16 + (MX ? 12 * a.stages : 0) <= 512 ? 2 : 1;
-    const uint32_t smem = a.off_meta + (uint32_t)round_up(meta, 16) + 1024;
+    const uint32_t smem = a.off_meta + meta + 1024;
 
     static PerDeviceOnce once;
     int sms = 0;
     const moe_status_t st = once.get(
         [](int *v) {
             if (cudaFuncSetAttribute(decode_kernel<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)kDecSmemMax - 1024) != cudaSuccess)
+                                     (int)kDecSmemMax - 2048) != cudaSuccess)
                 return MOE_ERR_CUDA;
             *v = device_sm_count();
             return MOE_OK;
@@ -952,7 +963,12 @@ DecArgs decode_args(const moe_bf16_t *x, const float *logits, const float *bias,
 
 extern "C" size_t moe_decode_workspace_bytes(int64_t T, int H, int F, int E, int k) {
     if (!moe::decode_sizes_ok(T, H, F, E, k)) return 0;
-    return moe::decode_layout(T, H, F, E, k).total;
+    size_t n = 0;
+    for (int64_t t = 0; t <= T; ++t) {   // fewer tokens may be cut finer
+        const size_t v = moe::decode_layout(t, H, F, E, k).total;
+        n = v > n ? v : n;
+    }
+    return n;
 }
 
 extern "C" moe_status_t moe_decode_workspace_init(void *ws, size_t ws_bytes, moe_stream_t stream) {
@@ -973,7 +989,7 @@ extern "C" moe_status_t moe_decode(const moe_bf16_t *x, const float *logits, con
     if (st != MOE_OK || T == 0) return st;
     if (!W_gate || !W_up || !W_down) return MOE_ERR_INVALID_ARG;
     if (!all_aligned16({W_gate, W_up, W_down, ws})) return MOE_ERR_UNSUPPORTED;
-    if (!ws || ws_bytes < moe_decode_workspace_bytes(T, H, F, E, k)) return MOE_ERR_WORKSPACE;
+    if (!ws || ws_bytes < decode_layout(T, H, F, E, k).total) return MOE_ERR_WORKSPACE;
     const moe_bf16_t *const W[3] = {W_gate, W_up, W_down};
     return launch_decode<false>(decode_args(x, logits, expert_bias, score_fn, normalize, cl, T, H, F, E, k, topk_idx,
                                             topk_w, out),
@@ -993,7 +1009,7 @@ extern "C" moe_status_t moe_decode_mxfp8(const moe_bf16_t *x, const float *logit
     if (st != MOE_OK || T == 0) return st;
     if (!Wg_q || !Wg_sf || !Wu_q || !Wu_sf || !Wd_q || !Wd_sf) return MOE_ERR_INVALID_ARG;
     if (!all_aligned16({Wg_q, Wg_sf, Wu_q, Wu_sf, Wd_q, Wd_sf, ws})) return MOE_ERR_UNSUPPORTED;
-    if (!ws || ws_bytes < moe_decode_workspace_bytes(T, H, F, E, k)) return MOE_ERR_WORKSPACE;
+    if (!ws || ws_bytes < decode_layout(T, H, F, E, k).total) return MOE_ERR_WORKSPACE;
     DecArgs a = decode_args(x, logits, expert_bias, score_fn, normalize, cl, T, H, F, E, k, topk_idx, topk_w, out);
     a.wq[0] = Wg_q;
     a.wsf[0] = Wg_sf;

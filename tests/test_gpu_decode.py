@@ -13,7 +13,7 @@ import torch
 from helpers import assert_close_rms
 from mixture_experts_ffn_warp_gb300 import (DecodeWorkspace, MoeDecode, MoeDecodeMX, MoeForward, MxWeights, moe_decode,
                                             moe_route_topk, moe_route_topk_sigmoid)
-from mixture_experts_ffn_warp_gb300._binding import MoeError
+from mixture_experts_ffn_warp_gb300._binding import DEVERR_TIMEOUT, MoeError
 
 pytestmark = pytest.mark.gpu
 TOL, TOL_MX = 2e-3, 6e-3
@@ -255,3 +255,22 @@ def test_refusals():
         DecodeWorkspace(65, H, F, E, k)
     with pytest.raises(ValueError):
         MoeDecode(T, H, F, E, k, router="hash")
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_wait_timeout_then_recovery(mx):
+    """With the device waits limited to 1 ns the call reports the timeout instead of finishing; after the
+    workspace is initialised again the same call is right (no trap, no hang, nothing left allocated)."""
+    T, H, F, E, k = 4, 512, 512, 8, 2
+    x, lg, W = make(T, H, F, E, seed=10)
+    mw = MxWeights(*W) if mx else None
+    m = (MoeDecodeMX if mx else MoeDecode)(T, H, F, E, k)
+    m.ws.set_wait_limit(1)
+    m(x, lg, mw) if mx else m(x, lg, *W)
+    torch.cuda.synchronize()
+    assert m.ws.read_error() & DEVERR_TIMEOUT
+    m.ws.reset()
+    out = m(x, lg, mw) if mx else m(x, lg, *W)
+    assert m.ws.read_error() == 0
+    idx, w = moe_route_topk(lg, k)
+    check(out, reference(x, mw.dequantized() if mx else W, idx, w), mx)
