@@ -145,6 +145,29 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple | None = 
     return t
 
 
+# The calls of a generation step are short (a few us): their argument checks and the stream
+# lookup below take the cheapest route to the same answers as _need and _stream.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, dev: int):
+    """The stream handle: `stream`, or the current one of device `dev`."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _addr(t, name: str, dtype: torch.dtype, shape: tuple, dev: int) -> int:
+    """The device address of a contiguous CUDA tensor of this dtype and shape on device `dev`."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous() and dev >= 0:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+
+
 # ------------------------------------------------------------------ workspace
 
 class Workspace:
@@ -694,32 +717,35 @@ class NormOutput:
                    rstd=buf(True, T, dtype=torch.float32))
 
 
+def _need2d(t, name: str, dtype: torch.dtype):
+    if not (isinstance(t, torch.Tensor) and t.dim() == 2 and t.get_device() >= 0):
+        _need(t, name, dtype)
+        raise ValueError(f"{name} must have two dimensions")
+
+
 def moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
                     out: NormOutput | None = None, bf16: bool = True, mxfp8: bool = False, stream=None) -> NormOutput:
     """sum = x + residual, y = sum * rstd * weight in bf16 and / or MXFP8 along H (moe.h).
     out: buffers of an earlier NormOutput.empty (which also says which outputs are wanted)."""
-    _need(x, "x", torch.bfloat16)
-    if x.dim() != 2:
-        raise ValueError("x must be [T, H]")
-    T, H = x.shape
-    dev = x.device
-    _need(weight, "weight", torch.bfloat16, (H,), dev)
-    if residual is not None:
-        _need(residual, "residual", torch.bfloat16, (T, H), dev)
+    _need2d(x, "x", torch.bfloat16)
+    T, H = rows = x.shape
+    dev = x.get_device()
     if out is None:
-        out = NormOutput.empty(T, H, bf16, mxfp8, residual is not None, dev)
-    else:
-        _need(out.rstd, "out.rstd", torch.float32, (T,), dev)
-        if residual is not None:
-            _need(out.sum, "out.sum", torch.bfloat16, (T, H), dev)
-        if out.y is not None:
-            _need(out.y, "out.y", torch.bfloat16, (T, H), dev)
-        if out.y_q is not None:
-            _need(out.y_q, "out.y_q", torch.uint8, (T, H), dev)
-            _need(out.y_sf, "out.y_sf", torch.uint8, (T, H // 32), dev)
-    _check("moe_add_rmsnorm", load_library().moe_add_rmsnorm(
-        _ptr(x), _ptr(residual), _ptr(weight), eps, T, H, _ptr(out.sum) if residual is not None else None,
-        _ptr(out.y), _ptr(out.y_q), _ptr(out.y_sf), _ptr(out.rstd), _stream(stream)))
+        out = NormOutput.empty(T, H, bf16, mxfp8, residual is not None, x.device)
+    r = s = y = q = sf = None
+    if residual is not None:
+        r = _addr(residual, "residual", torch.bfloat16, rows, dev)
+        s = _addr(out.sum, "out.sum", torch.bfloat16, rows, dev)
+    if out.y is not None:
+        y = _addr(out.y, "out.y", torch.bfloat16, rows, dev)
+    if out.y_q is not None:
+        q = _addr(out.y_q, "out.y_q", torch.uint8, rows, dev)
+        sf = _addr(out.y_sf, "out.y_sf", torch.uint8, (T, H // 32), dev)
+    st = load_library().moe_add_rmsnorm(
+        _addr(x, "x", torch.bfloat16, rows, dev), r, _addr(weight, "weight", torch.bfloat16, (H,), dev), eps, T, H, s, y,
+        q, sf, _addr(out.rstd, "out.rstd", torch.float32, (T,), dev), _stream_on(stream, dev))
+    if st:
+        raise MoeError("moe_add_rmsnorm", st)
     return out
 
 
@@ -740,28 +766,24 @@ def moe_add_rmsnorm_bwd(dy: torch.Tensor, sum: torch.Tensor, weight: torch.Tenso
                         want_dweight: bool = True, stream=None):
     """Gradient of moe_add_rmsnorm (moe.h): (dx bf16 [T, H] of x and the residual alike,
     dweight fp32 [H] or None).  sum: the forward's sum (its x where it had no residual)."""
-    _need(dy, "dy", torch.bfloat16)
-    if dy.dim() != 2:
-        raise ValueError("dy must be [T, H]")
-    T, H = dy.shape
-    dev = dy.device
-    _need(sum, "sum", torch.bfloat16, (T, H), dev)
-    _need(weight, "weight", torch.bfloat16, (H,), dev)
-    _need(rstd, "rstd", torch.float32, (T,), dev)
-    if d_sum is not None:
-        _need(d_sum, "d_sum", torch.bfloat16, (T, H), dev)
+    _need2d(dy, "dy", torch.bfloat16)
+    T, H = rows = dy.shape
+    dev = dy.get_device()
     if dx is None:
-        dx = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
-    _need(dx, "dx", torch.bfloat16, (T, H), dev)
+        dx = torch.empty(T, H, dtype=torch.bfloat16, device=dy.device)
     if dweight is None and want_dweight:
-        dweight = torch.empty(H, dtype=torch.float32, device=dev)
-    if dweight is not None:
-        _need(dweight, "dweight", torch.float32, (H,), dev)
-        if ws is None:
-            ws = NormWorkspace(T, H, dev)
-    _check("moe_add_rmsnorm_bwd", load_library().moe_add_rmsnorm_bwd(
-        _ptr(dy), _ptr(d_sum), _ptr(sum), _ptr(weight), _ptr(rstd), T, H, _ptr(dx), _ptr(dweight),
-        _ptr(ws.buf) if ws is not None else None, ws.nbytes if ws is not None else 0, _stream(stream)))
+        dweight = torch.empty(H, dtype=torch.float32, device=dy.device)
+    if dweight is not None and ws is None:
+        ws = NormWorkspace(T, H, dy.device)
+    st = load_library().moe_add_rmsnorm_bwd(
+        _addr(dy, "dy", torch.bfloat16, rows, dev),
+        None if d_sum is None else _addr(d_sum, "d_sum", torch.bfloat16, rows, dev),
+        _addr(sum, "sum", torch.bfloat16, rows, dev), _addr(weight, "weight", torch.bfloat16, (H,), dev),
+        _addr(rstd, "rstd", torch.float32, (T,), dev), T, H, _addr(dx, "dx", torch.bfloat16, rows, dev),
+        None if dweight is None else _addr(dweight, "dweight", torch.float32, (H,), dev),
+        None if ws is None else ws.buf.data_ptr(), 0 if ws is None else ws.nbytes, _stream_on(stream, dev))
+    if st:
+        raise MoeError("moe_add_rmsnorm_bwd", st)
     return dx, dweight
 
 
@@ -769,22 +791,20 @@ def moe_permute_rows_mxfp8(rows_q: torch.Tensor, rows_sf: torch.Tensor, topk_idx
                            out: PermutationMX | None = None, stream=None) -> PermutationMX:
     """moe_permute_mxfp8 for rows that are already MXFP8: codes uint8 [T, H], row-major
     scales uint8 [T, H/32] (moe.h)."""
-    _need(rows_q, "rows_q", torch.uint8)
-    if rows_q.dim() != 2:
-        raise ValueError("rows_q must be [T, H]")
+    _need2d(rows_q, "rows_q", torch.uint8)
+    _need2d(topk_idx, "topk_idx", torch.int32)
     T, H = rows_q.shape
-    dev = rows_q.device
-    _need(rows_sf, "rows_sf", torch.uint8, (T, H // 32), dev)
-    _need(topk_idx, "topk_idx", torch.int32, None, dev)
-    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
-        raise ValueError(f"topk_idx must be [{T}, k]")
     k = topk_idx.shape[1]
+    dev = rows_q.get_device()
     if out is None:
-        out = PermutationMX.empty(T, H, E, k, dev)
-    _check("moe_permute_rows_mxfp8", load_library().moe_permute_rows_mxfp8(
-        _ptr(rows_q), _ptr(rows_sf), _ptr(topk_idx), T, H, E, k, _ptr(out.x_q), _ptr(out.x_sf), out.rows_cap,
-        _ptr(out.dst_of_route), _ptr(out.src_of_row), _ptr(out.group_sizes), _ptr(out.group_offsets), _ptr(ws.buf),
-        ws.nbytes, _stream(stream)))
+        out = PermutationMX.empty(T, H, E, k, rows_q.device)
+    st = load_library().moe_permute_rows_mxfp8(
+        _addr(rows_q, "rows_q", torch.uint8, (T, H), dev), _addr(rows_sf, "rows_sf", torch.uint8, (T, H // 32), dev),
+        _addr(topk_idx, "topk_idx", torch.int32, (T, k), dev), T, H, E, k, out.x_q.data_ptr(), out.x_sf.data_ptr(),
+        out.rows_cap, out.dst_of_route.data_ptr(), out.src_of_row.data_ptr(), out.group_sizes.data_ptr(),
+        out.group_offsets.data_ptr(), ws.buf.data_ptr(), ws.nbytes, _stream_on(stream, dev))
+    if st:
+        raise MoeError("moe_permute_rows_mxfp8", st)
     return out
 
 
@@ -809,27 +829,29 @@ class DecodeWorkspace(Workspace):
             _ptr(self.buf), self.nbytes, _stream(stream)))
 
 
-def _decode_args(x, logits, expert_bias, score_fn, normalize, clamp, E, k, topk_idx, topk_w, out):
-    _need(x, "x", torch.bfloat16)
-    if x.dim() != 2:
-        raise ValueError("x must be [T, H]")
+_NO_CLAMP = (float("-inf"), float("inf"), float("-inf"), float("inf"))
+
+
+def _decode(fn, x, logits, weights, F, E, k, ws, score_fn, expert_bias, normalize, clamp, topk_idx, topk_w, out, stream):
+    """Checks and call shared by moe_decode and moe_decode_mxfp8; weights(H, dev): their addresses."""
+    _need2d(x, "x", torch.bfloat16)
     T, H = x.shape
-    dev = x.device
-    _need(logits, "logits", torch.float32, (T, E), dev)
-    if expert_bias is not None:
-        _need(expert_bias, "expert_bias", torch.float32, (E,), dev)
+    dev = x.get_device()
     if topk_idx is None:
-        topk_idx = torch.empty(T, k, dtype=torch.int32, device=dev)
+        topk_idx = torch.empty(T, k, dtype=torch.int32, device=x.device)
     if topk_w is None:
-        topk_w = torch.empty(T, k, dtype=torch.float32, device=dev)
+        topk_w = torch.empty(T, k, dtype=torch.float32, device=x.device)
     if out is None:
-        out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
-    _need(topk_idx, "topk_idx", torch.int32, (T, k), dev)
-    _need(topk_w, "topk_w", torch.float32, (T, k), dev)
-    _need(out, "out", torch.bfloat16, (T, H), dev)
-    lo, hi = float("-inf"), float("inf")
-    return T, H, topk_idx, topk_w, out, (_ptr(x), _ptr(logits), _ptr(expert_bias), int(score_fn),
-                                         int(bool(normalize)), *(clamp if clamp is not None else (lo, hi, lo, hi)))
+        out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+    st = getattr(load_library(), fn)(
+        _addr(x, "x", torch.bfloat16, (T, H), dev), _addr(logits, "logits", torch.float32, (T, E), dev),
+        None if expert_bias is None else _addr(expert_bias, "expert_bias", torch.float32, (E,), dev), score_fn,
+        1 if normalize else 0, *(_NO_CLAMP if clamp is None else clamp), *weights(H, dev), T, H, F, E, k,
+        _addr(topk_idx, "topk_idx", torch.int32, (T, k), dev), _addr(topk_w, "topk_w", torch.float32, (T, k), dev),
+        _addr(out, "out", torch.bfloat16, (T, H), dev), ws.buf.data_ptr(), ws.nbytes, _stream_on(stream, dev))
+    if st:
+        raise MoeError(fn, st)
+    return out, topk_idx, topk_w
 
 
 def moe_decode(x: torch.Tensor, logits: torch.Tensor, W_gate: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tensor,
@@ -837,18 +859,14 @@ def moe_decode(x: torch.Tensor, logits: torch.Tensor, W_gate: torch.Tensor, W_up
                clamp=None, topk_idx=None, topk_w=None, out=None, stream=None):
     """An MoE layer from logits to output for up to DECODE_MAX_TOKENS tokens (moe.h): (out
     bf16 [T, H], topk_idx, topk_w).  clamp = (gate_lo, gate_hi, up_lo, up_hi)."""
-    _need(W_gate, "W_gate", torch.bfloat16)
     if W_gate.dim() != 3:
         raise ValueError("W_gate must be [E, H, F]")
     E, _, F = W_gate.shape
-    T, H, topk_idx, topk_w, out, args = _decode_args(x, logits, expert_bias, score_fn, normalize, clamp, E, k, topk_idx,
-                                                     topk_w, out)
-    for name, w, shape in (("W_gate", W_gate, (E, H, F)), ("W_up", W_up, (E, H, F)), ("W_down", W_down, (E, F, H))):
-        _need(w, name, torch.bfloat16, shape, x.device)
-    _check("moe_decode", load_library().moe_decode(
-        *args, _ptr(W_gate), _ptr(W_up), _ptr(W_down), T, H, F, E, k, _ptr(topk_idx), _ptr(topk_w), _ptr(out),
-        _ptr(ws.buf), ws.nbytes, _stream(stream)))
-    return out, topk_idx, topk_w
+    return _decode("moe_decode", x, logits,
+                   lambda H, dev: (_addr(W_gate, "W_gate", torch.bfloat16, (E, H, F), dev),
+                                   _addr(W_up, "W_up", torch.bfloat16, (E, H, F), dev),
+                                   _addr(W_down, "W_down", torch.bfloat16, (E, F, H), dev)),
+                   F, E, k, ws, score_fn, expert_bias, normalize, clamp, topk_idx, topk_w, out, stream)
 
 
 def moe_decode_mxfp8(x: torch.Tensor, logits: torch.Tensor, Wg_q, Wg_sf, Wu_q, Wu_sf, Wd_q, Wd_sf, F: int, k: int,
@@ -856,12 +874,11 @@ def moe_decode_mxfp8(x: torch.Tensor, logits: torch.Tensor, Wg_q, Wg_sf, Wu_q, W
                      clamp=None, topk_idx=None, topk_w=None, out=None, stream=None):
     """moe_decode on MXFP8 expert weights (moe_quantize_weights_mxfp8's codes and scales; moe.h)."""
     E = logits.shape[-1]
-    T, H, topk_idx, topk_w, out, args = _decode_args(x, logits, expert_bias, score_fn, normalize, clamp, E, k, topk_idx,
-                                                     topk_w, out)
-    for name, t, n in (("Wg_q", Wg_q, 1), ("Wu_q", Wu_q, 1), ("Wd_q", Wd_q, 1), ("Wg_sf", Wg_sf, 32),
-                       ("Wu_sf", Wu_sf, 32), ("Wd_sf", Wd_sf, 32)):
-        _need(t, name, torch.uint8, (E * H * F // n,), x.device)
-    _check("moe_decode_mxfp8", load_library().moe_decode_mxfp8(
-        *args, _ptr(Wg_q), _ptr(Wg_sf), _ptr(Wu_q), _ptr(Wu_sf), _ptr(Wd_q), _ptr(Wd_sf), T, H, F, E, k,
-        _ptr(topk_idx), _ptr(topk_w), _ptr(out), _ptr(ws.buf), ws.nbytes, _stream(stream)))
-    return out, topk_idx, topk_w
+
+    def weights(H, dev):
+        n = E * H * F
+        return (_addr(Wg_q, "Wg_q", torch.uint8, (n,), dev), _addr(Wg_sf, "Wg_sf", torch.uint8, (n // 32,), dev),
+                _addr(Wu_q, "Wu_q", torch.uint8, (n,), dev), _addr(Wu_sf, "Wu_sf", torch.uint8, (n // 32,), dev),
+                _addr(Wd_q, "Wd_q", torch.uint8, (n,), dev), _addr(Wd_sf, "Wd_sf", torch.uint8, (n // 32,), dev))
+    return _decode("moe_decode_mxfp8", x, logits, weights, F, E, k, ws, score_fn, expert_bias, normalize, clamp,
+                   topk_idx, topk_w, out, stream)

@@ -72,19 +72,21 @@ struct Counters {
 };
 constexpr size_t kDecCtrBytes = (sizeof(Counters) + 1023) / 1024 * 1024;
 
-// Pieces that the K range of a tile is cut into (a rule on the sizes and the number of experts
-// hit, so that it is the same wherever the call runs): about 8 segments per CTA, and finer
-// ones for the down product of the last expert, whose end is the call's end.  More tokens
-// make a segment's partial sums larger: the shortest piece grows with them.  
+// Pieces that the K range of a tile is cut into: a rule on the sizes and the number of experts
+// hit, so that the order of the sums is the same wherever the call runs.  About 8 segments per
+// CTA; the down segments of the last `tail` experts, whose end is the call's end, are four times
+// finer, and `tail` is large enough for every CTA to spend one of the long segments on them.
+// More tokens make a segment's partial sums larger: the shortest piece grows with them.
 struct Pieces {
-    int up, down, last;
+    int up, down, last, tail;
 };
 __host__ __device__ inline Pieces pieces_of(int A, int FT, int NT, int K1, int K2, int T) {
     const int64_t per_cta = (int64_t)A * ((int64_t)FT * K1 + (int64_t)NT * K2) / kDecMaxCtas;
     const int lo = 1 + T / 16;
     const int64_t c = per_cta / 8, f = per_cta / 32;
     const int p = (int)(c < lo ? lo : c > 64 ? 64 : c), l = (int)(f < lo ? lo : f > 8 ? 8 : f);
-    return Pieces{(K1 + p - 1) / p, (K2 + p - 1) / p, (K2 + l - 1) / l};
+    const int tail = (int)(((int64_t)p * kDecMaxCtas + (int64_t)NT * K2 - 1) / ((int64_t)NT * K2));
+    return Pieces{(K1 + p - 1) / p, (K2 + p - 1) / p, (K2 + l - 1) / l, tail < A ? tail : A};
 }
 
 struct DecArgs {
@@ -437,7 +439,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     const int FT = a.F / 128, K1 = a.H / KC, K2 = a.F / KC, NT = (a.H + 255) / 256;
     const Pieces pc = pieces_of(A, FT, NT, K1, K2, a.T);
     const int S2 = pc.down > pc.last ? pc.down : pc.last;   // pieces that part2 has room for
-    const int n_up = A * FT * pc.up, n_down = (A - 1) * NT * pc.down + NT * pc.last;
+    const int head = A - pc.tail;                          // experts whose down segments are the long ones
+    const int n_up = A * FT * pc.up, n_down = head * NT * pc.down + pc.tail * NT * pc.last;
     const uint32_t row_bytes = MX ? 2u * a.F : 4u * a.F;    // bytes of h per padded row, both terms
     auto h_block = [&](int ai, int c16, int kc) {           // block kc of the expert's h
         const uint32_t bytes = (uint32_t)c16 * 256 + (MX ? kSfBytes : 0);
@@ -463,14 +466,17 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
                     S = pc.up;
                     K = K1;
                 } else {
-                    const int d = q - n_up, before = (A - 1) * NT * pc.down;
+                    int d = q - n_up;
                     s.down = d < n_down ? 1 : -1;
-                    s.ai = d < before ? d / (NT * pc.down) : A - 1;
-                    const int rem = d - s.ai * NT * pc.down;
+                    const bool fine = d >= head * NT * pc.down;
+                    if (fine) d -= head * NT * pc.down;
+                    S = fine ? pc.last : pc.down;
+                    K = K2;
+                    s.ai = d / (NT * S);
+                    const int rem = d - s.ai * NT * S;
+                    if (fine) s.ai += head;
                     s.piece = rem / NT;
                     s.tile = rem - s.piece * NT;
-                    S = d < before ? pc.down : pc.last;
-                    K = K2;
                 }
                 if (s.down >= 0) {
                     s.e = s_active[s.ai];
@@ -780,7 +786,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     __syncthreads();
     if (s_joined) {
         // a thread group of g lanes adds 4 columns of one token over its experts and their pieces
-        const int quads = a.T * (a.H / 4), threads = G * kDecThreads, last_r0 = s_r0[A - 1];
+        const int quads = a.T * (a.H / 4), threads = G * kDecThreads, last_r0 = head < A ? s_r0[head] : R;
         int g = 1;
         while (g < 32 && quads * g * 2 <= threads) g *= 2;
         const int sub = lane & (g - 1);
