@@ -48,6 +48,7 @@ namespace {
 
 constexpr int kDecWarps = 12;        // weights, x / h, MMA, idle, 4 drain, 4 join
 constexpr int kDecThreads = kDecWarps * 32;
+constexpr int kRouteWarps = kDecWarps - 1;   // all but the one that sets up
 constexpr int kDecMaxStages = 8;
 constexpr int kDecMaxCtas = 160;
 constexpr int kDecMaxExperts = 1024;
@@ -198,6 +199,10 @@ __device__ __forceinline__ uint32_t order_key(float v) {   // larger ranks first
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+__device__ __forceinline__ float key_value(uint32_t key) {   // the value that order_key was made of
+    return __uint_as_float(key == 1u ? 0x7FC00000u : (key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
+}
+
 // E4M3 code of v / 2^X and the remainder v - code * 2^X; what is not finite becomes a NaN code.
 __device__ __forceinline__ uint8_t e4m3_term(float v, int X, float &rem) {
     const __nv_fp8_storage_t c = __nv_cvt_float_to_fp8(v * mx::inv_pow2(X), __NV_SATFINITE, __NV_E4M3);
@@ -246,36 +251,39 @@ struct Seg {
     int r0;            // routes of the experts before it
 };
 
-// Top-k routing of tokens warp, warp + kDecWarps, ... into shared memory: each lane holds experts
+// Top-k routing of tokens w, w + kRouteWarps, ... into shared memory: each lane holds experts
 // lane, lane + 32, ... (V of them) in registers.  `meanwhile` runs while the first token's
 // logits are on their way.
 template <int V, typename F>
-__device__ __forceinline__ void route_tokens(const DecArgs &a, int warp, int lane, bool write, uint64_t *s_mask,
+__device__ __forceinline__ void route_tokens(const DecArgs &a, int w, int lane, bool write, uint32_t *s_mask,
                                              uint16_t *s_idx, float *s_w, F &&meanwhile) {
-    float v[V], bias[V];
-    auto load = [&](int t, float (&to)[V]) {
+    float next[V], bias[V];
+    auto load = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) to[i] = lane + 32 * i < a.E ? __ldg(a.logits + (int64_t)t * a.E + lane + 32 * i) : 0.0f;
+        for (int i = 0; i < V; ++i)
+            next[i] = lane + 32 * i < a.E ? __ldg(a.logits + (int64_t)t * a.E + lane + 32 * i) : 0.0f;
     };
-    if (warp < a.T) load(warp, v);
+    if (w < a.T) load(w);
     if (a.sigmoid) {
 #pragma unroll
         for (int i = 0; i < V; ++i) bias[i] = a.bias && lane + 32 * i < a.E ? __ldg(a.bias + lane + 32 * i) : 0.0f;
     }
     meanwhile();
-    for (int t = warp; t < a.T; t += kDecWarps) {
+    for (int t = w; t < a.T; t += kRouteWarps) {
         uint32_t key[V];
+        float score[V];                                // sigmoid: the unbiased score
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float s = v[i];
+            float r = next[i];
             if (a.sigmoid) {
-                s = 1.0f / (1.0f + expf(-s));
-                if (a.bias) s += bias[i];
+                score[i] = 1.0f / (1.0f + expf(-r));
+                r = a.bias ? score[i] + bias[i] : score[i];
             }
-            key[i] = lane + 32 * i < a.E ? order_key(s) : 0u;
+            key[i] = lane + 32 * i < a.E ? order_key(r) : 0u;
         }
-        if (t + kDecWarps < a.T) load(t + kDecWarps, v);
-        int mine = 0;                                  // lane j keeps the expert of slot j
+        if (t + kRouteWarps < a.T) load(t + kRouteWarps);
+        int mine = 0;                                  // lane j keeps slot j: the expert, its logit or score
+        float val = 0.0f;
         for (int j = 0; j < a.k; ++j) {
             uint32_t bk = key[0];
             int bi = 0;
@@ -284,35 +292,41 @@ __device__ __forceinline__ void route_tokens(const DecArgs &a, int warp, int lan
                 if (key[i] > bk) { bk = key[i]; bi = i; }
             const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, bk);
             const int e = (int)__reduce_min_sync(0xFFFFFFFFu, bk == top ? (uint32_t)(lane + 32 * bi) : 0xFFFFFFFFu);
-            if (lane == j) mine = e;
+            float x = key_value(top);
+            if (a.sigmoid) {
+                float sc = score[0];
+#pragma unroll
+                for (int i = 1; i < V; ++i)
+                    if (bi == i) sc = score[i];
+                x = __shfl_sync(0xFFFFFFFFu, sc, e & 31);
+            }
+            if (lane == j) { mine = e; val = x; }
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (e == lane + 32 * i) key[i] = 0;
         }
-        const float l = lane < a.k ? __ldg(a.logits + (int64_t)t * a.E + mine) : 0.0f;
-        float w;
+        float wt;
         if (a.sigmoid) {
-            float sc = lane < a.k ? 1.0f / (1.0f + expf(-l)) : 0.0f;
-            if (sc != sc) sc = 0.0f;                   // a NaN logit scores 0
+            const float sc = lane < a.k && val == val ? val : 0.0f;   // a NaN logit scores 0
             float S = sc;
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) S += __shfl_xor_sync(0xFFFFFFFFu, S, off);
-            w = a.normalize ? sc / (S + 1e-20f) : sc;
+            wt = a.normalize ? sc / (S + 1e-20f) : sc;
         } else {
-            const float l0 = __shfl_sync(0xFFFFFFFFu, l, 0);
-            const float ex = (lane < a.k && l0 != -INFINITY) ? expf(l - l0) : 0.0f;
+            const float l0 = __shfl_sync(0xFFFFFFFFu, val, 0);
+            const float ex = (lane < a.k && l0 != -INFINITY) ? expf(val - l0) : 0.0f;
             float S = ex;
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) S += __shfl_xor_sync(0xFFFFFFFFu, S, off);
-            w = l0 == -INFINITY ? 0.0f : ex / S;
+            wt = l0 == -INFINITY ? 0.0f : ex / S;
         }
         if (lane < a.k) {
             s_idx[t * a.k + lane] = (uint16_t)mine;
-            s_w[t * a.k + lane] = w;
-            atomicOr(reinterpret_cast<unsigned long long *>(&s_mask[mine]), 1ull << t);
+            s_w[t * a.k + lane] = wt;
+            atomicOr(&s_mask[2 * mine + (t >> 5)], 1u << (t & 31));
             if (write) {
                 a.topk_idx[t * a.k + lane] = mine;
-                a.topk_w[t * a.k + lane] = w;
+                a.topk_w[t * a.k + lane] = wt;
             }
         }
     }
@@ -329,7 +343,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     __shared__ uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
     __shared__ Seg s_seg[kSegSlots];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_active_n, s_joined;
+    __shared__ int s_joined;
+    __shared__ int s_chunk_n[kDecMaxExperts / 32], s_chunk_sum[kDecMaxExperts / 32];
     __shared__ volatile int s_abort;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -350,91 +365,109 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     // ------------------------------------------------------------ set-up and routing
     const uint32_t epoch = __ldcg(&a.ctr->epoch);
     CounterSet *ctr = &a.ctr->set[epoch & 1];
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < a.stages; ++s) {
-            sm100::mbar_init(&full_w[s], 1);
-            sm100::mbar_init(&full_b[s], 1);
-            sm100::mbar_init(&empty[s], 1);
+    // Warp 3, which has no role, sets up barriers and TMEM; the others route, every CTA for
+    // itself.  Meanwhile (MXFP8): this CTA's share of x, blocks of 32 elements, a warp each,
+    // into [H / 128] blocks of 2 T16 operand rows (first terms, then second) and a scale atom.
+    if (warp == 3) {
+        if (lane == 0) {
+            for (int s = 0; s < a.stages; ++s) {
+                sm100::mbar_init(&full_w[s], 1);
+                sm100::mbar_init(&full_b[s], 1);
+                sm100::mbar_init(&empty[s], 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                sm100::mbar_init(&tfull[i], 1);
+                sm100::mbar_init(&tempty[i], 128);
+            }
+            for (int i = 0; i < kSegSlots; ++i) {
+                sm100::mbar_init(&seg_full[i], 1);
+                sm100::mbar_init(&seg_empty[i], 6);    // x / h, MMA, four drain warps
+            }
+            sm100::mbar_init(&drain, 1);
+            s_abort = 0;
+            sm100::fence_mbar_init();
+            if (!MX) {
+                sm100::prefetch_tmap(&tmX);
+                sm100::prefetch_tmap(&tmG);
+                sm100::prefetch_tmap(&tmU);
+                sm100::prefetch_tmap(&tmD);
+            }
         }
-        for (int i = 0; i < 2; ++i) {
-            sm100::mbar_init(&tfull[i], 1);
-            sm100::mbar_init(&tempty[i], 128);
-        }
-        for (int i = 0; i < kSegSlots; ++i) {
-            sm100::mbar_init(&seg_full[i], 1);
-            sm100::mbar_init(&seg_empty[i], 6);        // x / h, MMA, four drain warps
-        }
-        sm100::mbar_init(&drain, 1);
-        s_abort = 0;
-        sm100::fence_mbar_init();
-    }
-    if (warp == 2) {
+        __syncwarp();
         sm100::tmem_alloc(&s_tmem, 512);
         sm100::tmem_relinquish();
-    }
-    for (int e = threadIdx.x; e < a.E; e += kDecThreads) s_mask[e] = 0;
-
-    // Every CTA routes for itself.  Meanwhile (MXFP8): this CTA's share of x, blocks of 32
-    // elements, a warp each, into [H / 128] blocks of 2 T16 operand rows (first terms, then
-    // second) and a scale atom.
-    auto meanwhile = [&]() {
-        if constexpr (MX) {
-            const int nb = a.H / 32;
-            const uint32_t blk_bytes = (uint32_t)a.T16 * 256 + kSfBytes;
-            for (int b = cta * kDecWarps + warp; b < a.T * nb; b += G * kDecWarps) {
-                const int t = b / nb, kb = b - t * nb;
-                uint8_t code[2], sf[2];
-                two_terms(__bfloat162float(a.x[(int64_t)t * a.H + kb * 32 + lane]), code, sf);
-                uint8_t *blk = a.xq + (size_t)(kb / 4) * blk_bytes;
+    } else {
+        const int rw = warp < 3 ? warp : warp - 1;
+        for (int e = rw * 32 + lane; e < a.E; e += kRouteWarps * 32) s_mask[e] = 0;
+        auto meanwhile = [&]() {
+            if constexpr (MX) {
+                const int nb = a.H / 32;
+                const uint32_t blk_bytes = (uint32_t)a.T16 * 256 + kSfBytes;
+                for (int b = cta * kRouteWarps + rw; b < a.T * nb; b += G * kRouteWarps) {
+                    const int t = b / nb, kb = b - t * nb;
+                    uint8_t code[2], sf[2];
+                    two_terms(__bfloat162float(a.x[(int64_t)t * a.H + kb * 32 + lane]), code, sf);
+                    uint8_t *blk = a.xq + (size_t)(kb / 4) * blk_bytes;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t n = t + i * a.T16;
-                    blk[sw128(n, (kb & 3) * 32 + lane)] = code[i];
-                    if (lane == 0) blk[a.T16 * 256 + sf_byte(n, kb & 3)] = sf[i];
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t n = t + i * a.T16;
+                        blk[sw128(n, (kb & 3) * 32 + lane)] = code[i];
+                        if (lane == 0) blk[a.T16 * 256 + sf_byte(n, kb & 3)] = sf[i];
+                    }
                 }
+                fence_proxy_async_global();
             }
-            fence_proxy_async_global();
-        }
-        sm100::tc_fence_before();
-        __syncthreads();
-        sm100::tc_fence_after();
-        if (MX && threadIdx.x == 0) count_release(&ctr->x_ready, 1);
-    };
-    if (a.E <= 64) route_tokens<2>(a, warp, lane, cta == 0, s_mask, s_idx, s_w, meanwhile);
-    else if (a.E <= 256) route_tokens<8>(a, warp, lane, cta == 0, s_mask, s_idx, s_w, meanwhile);
-    else route_tokens<32>(a, warp, lane, cta == 0, s_mask, s_idx, s_w, meanwhile);
+            asm volatile("barrier.cta.sync 3, %0;" ::"n"(kRouteWarps * 32) : "memory");
+            if (MX && threadIdx.x == 0) count_release(&ctr->x_ready, 1);
+        };
+        uint32_t *mask32 = reinterpret_cast<uint32_t *>(s_mask);
+        if (a.E <= 64) route_tokens<2>(a, rw, lane, cta == 0, mask32, s_idx, s_w, meanwhile);
+        else if (a.E <= 128) route_tokens<4>(a, rw, lane, cta == 0, mask32, s_idx, s_w, meanwhile);
+        else if (a.E <= 256) route_tokens<8>(a, rw, lane, cta == 0, mask32, s_idx, s_w, meanwhile);
+        else route_tokens<32>(a, rw, lane, cta == 0, mask32, s_idx, s_w, meanwhile);
+    }
+    sm100::tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
-        // the experts that are hit, ascending, with the routes and the 16-row blocks of h before each
-        int n = 0, rows = 0, routes = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane;
-            const uint64_t m = e < a.E ? s_mask[e] : 0;
-            const uint32_t hit = __ballot_sync(0xFFFFFFFFu, m != 0);
-            if (!hit) continue;
-            const int c = __popcll(m), mine = (c << 16) | ((c + 15) & ~15);   // both sums at once: each below 2^16
-            int incl = mine;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
-                if (lane >= off) incl += o;
-            }
-            if (m) {
-                const int i = n + __popc(hit & ((1u << lane) - 1));
-                s_active[i] = (uint16_t)e;
-                s_row0[i] = rows + ((incl - mine) & 0xFFFF);
-                s_r0[i] = routes + ((incl - mine) >> 16);
-            }
-            const int sum = __shfl_sync(0xFFFFFFFFu, incl, 31);
-            n += __popc(hit);
-            rows += sum & 0xFFFF;
-            routes += sum >> 16;
+    sm100::tc_fence_after();
+    // The experts that are hit, ascending, with the routes and the 16-row blocks of h before each:
+    // 32 experts a warp, their totals first.  (Routes and padded rows are summed in one word:
+    // 64 tokens * 32 experts keep each half below 2^16 within a chunk.)
+    const int chunks = (a.E + 31) / 32;
+    auto hit_of = [&](int e) { return e < a.E ? __popcll(s_mask[e]) : 0; };
+    for (int c = warp; c < chunks; c += kDecWarps) {
+        const int cnt = hit_of(c * 32 + lane);
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, cnt != 0));
+        const int sum = (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)((cnt << 16) | ((cnt + 15) & ~15)));
+        if (lane == 0) {
+            s_chunk_n[c] = n;
+            s_chunk_sum[c] = sum;
         }
-        if (lane == 0) s_active_n = n;
+    }
+    __syncthreads();
+    const int chunk_n = lane < chunks ? s_chunk_n[lane] : 0;
+    const int A = (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)chunk_n);
+    for (int c = warp; c < chunks; c += kDecWarps) {
+        const int before = lane < c ? s_chunk_sum[lane] : 0;
+        const int n0 = (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)(lane < c ? chunk_n : 0));
+        const int rows0 = (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)(before & 0xFFFF));
+        const int routes0 = (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)(before >> 16));
+        const int cnt = hit_of(c * 32 + lane), mine = (cnt << 16) | ((cnt + 15) & ~15);
+        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, cnt != 0);
+        int incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+            if (lane >= off) incl += o;
+        }
+        if (cnt) {
+            const int i = n0 + __popc(hit & ((1u << lane) - 1));
+            s_active[i] = (uint16_t)(c * 32 + lane);
+            s_row0[i] = rows0 + ((incl - mine) & 0xFFFF);
+            s_r0[i] = routes0 + ((incl - mine) >> 16);
+        }
     }
     __syncthreads();
 
-    const int A = s_active_n;
     const uint32_t tmem = s_tmem;
     const int FT = a.F / 128, K1 = a.H / KC, K2 = a.F / KC, NT = (a.H + 255) / 256;
     const Pieces pc = pieces_of(A, FT, NT, K1, K2, a.T);
