@@ -9,186 +9,371 @@
 //   dx = rstd (w dy - xhat mean(w dy xhat)) + d_s      (of x and of r alike)
 //   dw = sum over rows of dy xhat
 //
-// Bound by memory: each tensor is read or written once.  One block per row, the row held in
-// registers between the sum of squares and the scaling.
+// Bound by memory: each tensor is read or written once.  A thread owns V vectors of 8 columns
+// of every row its block takes, keeps their weights in registers and copies its own parts
+// of the next S - 1 rows to shared memory ahead of time (cp.async), so that the one barrier a
+// row, of the row sum, hides behind them; blocks stay for several rows.  Threads per block
+// follow from H, so that no lane idles.  (V, S, blocks per SM) are chosen by H; measured on
+// GB300, all of them swept, 8192 rows (16384 of 2048), against bytes / 6760 GB/s:
+//   forward, bf16 out     H = 2048: 41.6 us (39.7)   4096: 41.3 (39.7)   7168: 72.4 (69.5)
+//   forward, both outputs H = 2048: 47.8 us (44.8)   4096: 47.0 (44.8)   7168: 79.5 (78.5)
+//   backward without dw's last sum  H = 2048: 40.8 (39.7)  4096: 41.7 (39.7)  7168: 75.8 (69.5)
+// One block per row with the rows in registers took 89 us (7168, both outputs), the backward with
+// 256 threads, two vectors each and four rows ahead 57 us (4096).
+// sum may be x or r, dx may be dy or d_s: a row is read before it is written.
 #include "common.cuh"
 #include "mx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kNormThreads = 256;
-constexpr int kNormMaxVec = 16;      // 8-element vectors a thread holds: H <= 32768
-constexpr int kNormBwdBlocks = 304;  // rows of partial weight gradients
+constexpr int kNormMaxH = 32768;
+constexpr int kNormSms = 152;        // blocks are counted in multiples of this (dw's sum follows them)
+constexpr int kNormMaxThreads = 512;
 
-__device__ __forceinline__ void unpack8(const uint4 &raw, float (&v)[8]) {
+// Packed pairs of fp32 (one instruction for two operations).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)),
+          "l"(reinterpret_cast<const uint64_t &>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
+    return d;
+}
+__device__ __forceinline__ void unpack4(const uint4 &raw, float2 (&v)[4]) {
     const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&raw);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __bfloat1622float2(p[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
+    for (int i = 0; i < 4; ++i) v[i] = __bfloat1622float2(p[i]);
 }
-
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+__device__ __forceinline__ uint4 pack4(const float2 (&v)[4]) {
     uint4 raw;
     __nv_bfloat162 *p = reinterpret_cast<__nv_bfloat162 *>(&raw);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) p[i] = __float22bfloat162_rn(v[i]);
     return raw;
 }
 
-// Sum over the block, the same value in every thread; s_red holds one float per warp and is
-// free again after the caller's next __syncthreads.
+// Sum over the block, the same value in every thread; s_red holds one float per warp (the unused
+// ones zero) and is free again after the caller's next barrier.
 __device__ __forceinline__ float block_sum(float v, float *s_red) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
-    const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) s_red[warp] = v;
+    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
     __syncthreads();
+    const float4 *r = reinterpret_cast<const float4 *>(s_red);
     float t = 0.0f;
-    for (int i = 0; i < nw; ++i) t += s_red[i];
+    for (int i = 0; i < (int)(blockDim.x + 127) / 128; ++i) t += (r[i].x + r[i].y) + (r[i].z + r[i].w);
     return t;
 }
 
-template <int V>
-__global__ void __launch_bounds__(kNormThreads)
-add_rmsnorm_kernel(const uint4 *__restrict__ x, const uint4 *__restrict__ res, const uint4 *__restrict__ weight,
-                   float eps, int H, uint4 *__restrict__ sum, uint4 *__restrict__ y, uint8_t *__restrict__ y_q,
-                   uint8_t *__restrict__ y_sf, float *__restrict__ rstd_out) {
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ...; S rows of x and r in shared memory.
+template <int V, int S>
+__global__ void __launch_bounds__(kNormMaxThreads)
+add_rmsnorm_kernel(const uint4 *x, const uint4 *res, const uint4 *__restrict__ weight,
+                   float eps, int64_t T, int H, uint4 *sum, uint4 *__restrict__ y,
+                   uint8_t *__restrict__ y_q, uint8_t *__restrict__ y_sf, float *__restrict__ rstd_out) {
+    extern __shared__ uint4 s_rows[];   // [S][2][V][threads]
+    __shared__ __align__(16) float s_red[2][kNormMaxThreads / 32];
+    const int nv = H / 8, tid = threadIdx.x, NT = blockDim.x;
+    if (tid < 2 * kNormMaxThreads / 32) s_red[0][tid] = 0.0f;
+    __syncthreads();
     pdl_wait();
-    __shared__ float s_red[kNormThreads / 32];
-    const int nv = H / 8;
-    const int64_t row = blockIdx.x;
-    float v[V][8];
-    float ss = 0.0f;
+    auto slot = [&](int st, int tensor, int i) -> uint4 * { return s_rows + ((st * 2 + tensor) * V + i) * NT + tid; };
+    auto fetch = [&](int64_t row, int st) {
+        if (row < T) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = i * kNormThreads + threadIdx.x;
-        if (c < nv) {
-            unpack8(x[row * nv + c], v[i]);
-            if (res) {
-                float r[8];
-                unpack8(res[row * nv + c], r);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] += r[j];
-                sum[row * nv + c] = pack8(v[i]);
+            for (int i = 0; i < V; ++i) {
+                const int c = i * NT + tid;
+                if (c < nv) {
+                    cp_async16(slot(st, 0, i), x + row * nv + c);
+                    if (res) cp_async16(slot(st, 1, i), res + row * nv + c);
+                }
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
         }
-    }
-    ss = block_sum(ss, s_red);
-    const float rstd = 1.0f / sqrtf(ss / (float)H + eps);
-    if (threadIdx.x == 0 && rstd_out) rstd_out[row] = rstd;
+        cp_async_commit();   // (an empty group past the last row keeps the count)
+    };
+    const int64_t step = gridDim.x;
+    int64_t row = blockIdx.x;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = i * kNormThreads + threadIdx.x;
-        float o[8] = {};
-        if (c < nv) {
-            float w[8];
-            unpack8(weight[c], w);
+    for (int p = 0; p < S - 1; ++p) fetch(row + p * step, p);
+    uint4 w[V];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = v[i][j] * rstd * w[j];
-            if (y) y[row * nv + c] = pack8(o);
-        }
-        if (y_q) {
-            // four neighbouring threads hold one block of 32
-            float a = 0.0f;
+    for (int i = 0; i < V; ++i) w[i] = i * NT + tid < nv ? __ldg(weight + i * NT + tid) : make_uint4(0, 0, 0, 0);
+    const float inv_h = 1.0f / (float)H;
+    int par = 0, st = 0;
+    for (; row < T; row += step, par ^= 1) {
+        fetch(row + (S - 1) * step, st + S - 1 < S ? st + S - 1 : st - 1);
+        cp_async_wait<S - 1>();
+        float2 v[V][4];
+        float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(o[j]));
-            a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
-            a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
-            const int X = mx::scale_exp(a);
+        for (int i = 0; i < V; ++i) {
+            const int c = i * NT + tid;
             if (c < nv) {
-                *reinterpret_cast<uint2 *>(y_q + row * H + (int64_t)c * 8) = mx::quantize8(o, X);
-                if ((threadIdx.x & 3) == 0) y_sf[row * (H / 32) + c / 4] = (uint8_t)(X + 127);
+                unpack4(*slot(st, 0, i), v[i]);
+                if (res) {
+                    float2 r[4];
+                    unpack4(*slot(st, 1, i), r);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[i][j] = add2(v[i][j], r[j]);
+                    sum[row * nv + c] = pack4(v[i]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc = fma2(v[i][j], v[i][j], acc);
             }
         }
+        const float ss = block_sum(acc.x + acc.y, s_red[par]);   // the other half is free: one barrier a row
+        const float rstd = 1.0f / sqrtf(ss * inv_h + eps);
+        if (tid == 0 && rstd_out) rstd_out[row] = rstd;
+        const float2 rr = make_float2(rstd, rstd);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = i * NT + tid;
+            float2 o[4] = {};
+            if (c < nv) {
+                float2 wf[4];
+                unpack4(w[i], wf);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[j] = mul2(mul2(v[i][j], rr), wf[j]);
+                if (y) y[row * nv + c] = pack4(o);
+            }
+            if (y_q) {
+                // four neighbouring threads hold one block of 32
+                float a = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) a = fmaxf(a, fmaxf(fabsf(o[j].x), fabsf(o[j].y)));
+                a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
+                a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
+                const int X = mx::scale_exp(a);
+                if (c < nv) {
+                    float f[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        f[2 * j] = o[j].x;
+                        f[2 * j + 1] = o[j].y;
+                    }
+                    *reinterpret_cast<uint2 *>(y_q + row * H + (int64_t)c * 8) = mx::quantize8(f, X);
+                    if ((tid & 3) == 0) y_sf[row * (H / 32) + c / 4] = (uint8_t)(X + 127);
+                }
+            }
+        }
+        st = st + 1 < S ? st + 1 : 0;
     }
 }
 
-// dx of the rows blockIdx.x, blockIdx.x + gridDim.x, ..., and this block's share of dw.
-template <int V>
-__global__ void __launch_bounds__(kNormThreads)
-add_rmsnorm_bwd_kernel(const uint4 *__restrict__ dy, const uint4 *__restrict__ d_sum, const uint4 *__restrict__ sum,
+// dx of the rows blockIdx.x, blockIdx.x + gridDim.x, ..., and this block's share of dw, summed
+// in registers over its rows.  Up to V = 2 a thread keeps the products w dy and the row's s
+// between the dot product and dx; above, it reads them again from shared memory.
+template <int V, int S>
+__global__ void __launch_bounds__(kNormMaxThreads)
+add_rmsnorm_bwd_kernel(const uint4 *dy, const uint4 *d_sum, const uint4 *__restrict__ sum,
                        const uint4 *__restrict__ weight, const float *__restrict__ rstd_in, int64_t T, int H,
-                       uint4 *__restrict__ dx, float *__restrict__ dw_part) {
+                       uint4 *dx, float *__restrict__ dw_part) {
+    constexpr bool KEEP = V <= 2;
+    constexpr int KV = KEEP ? V : 1;
+    extern __shared__ uint4 s_rows[];   // [S][3][V][threads]
+    __shared__ __align__(16) float s_red[2][kNormMaxThreads / 32];
+    const int nv = H / 8, tid = threadIdx.x, NT = blockDim.x;
+    if (tid < 2 * kNormMaxThreads / 32) s_red[0][tid] = 0.0f;
+    __syncthreads();
     pdl_wait();
-    __shared__ float s_red[2][kNormThreads / 32];
-    const int nv = H / 8;
-    float dw[V][8];
+    auto slot = [&](int st, int tensor, int i) -> uint4 * { return s_rows + ((st * 3 + tensor) * V + i) * NT + tid; };
+    auto fetch = [&](int64_t row, int st) {
+        if (row < T) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
-    int par = 0;
-    for (int64_t row = blockIdx.x; row < T; row += gridDim.x, par ^= 1) {
-        const float rstd = rstd_in[row];
-        float g[V][8], xh[V][8];
-        float dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = i * kNormThreads + threadIdx.x;
-            if (c < nv) {
-                float w[8];
-                unpack8(dy[row * nv + c], g[i]);
-                unpack8(sum[row * nv + c], xh[i]);
-                unpack8(weight[c], w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    xh[i][j] *= rstd;
-                    dw[i][j] += g[i][j] * xh[i][j];
-                    g[i][j] *= w[j];
-                    dot += g[i][j] * xh[i][j];
+            for (int i = 0; i < V; ++i) {
+                const int c = i * NT + tid;
+                if (c < nv) {
+                    cp_async16(slot(st, 0, i), dy + row * nv + c);
+                    cp_async16(slot(st, 1, i), sum + row * nv + c);
+                    if (d_sum) cp_async16(slot(st, 2, i), d_sum + row * nv + c);
                 }
             }
         }
-        const float m = block_sum(dot, s_red[par]) / (float)H;   // the other half is free: one barrier a row
+        cp_async_commit();   // (an empty group past the last row keeps the count)
+    };
+    const int64_t step = gridDim.x;
+    int64_t row = blockIdx.x;
+#pragma unroll
+    for (int p = 0; p < S - 1; ++p) fetch(row + p * step, p);
+    uint4 w[V];
+    float2 dw[V][4];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        w[i] = i * NT + tid < nv ? __ldg(weight + i * NT + tid) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dw[i][j] = make_float2(0.0f, 0.0f);
+    }
+    float rstd = row < T ? __ldg(rstd_in + row) : 0.0f;
+    const float inv_h = 1.0f / (float)H;
+    int par = 0, st = 0;
+    for (; row < T; row += step, par ^= 1) {
+        fetch(row + (S - 1) * step, st + S - 1 < S ? st + S - 1 : st - 1);
+        const float rstd_next = row + step < T ? __ldg(rstd_in + row + step) : 0.0f;
+        cp_async_wait<S - 1>();
+        const float2 rr = make_float2(rstd, rstd);
+        float2 kept_g[KV][4], kept_x[KV][4];
+        float2 dot = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = i * kNormThreads + threadIdx.x;
-            if (c < nv) {
-                float o[8];
+            if (i * NT + tid < nv) {
+                float2 g[4], xv[4], wf[4];
+                unpack4(*slot(st, 0, i), g);
+                unpack4(*slot(st, 1, i), xv);
+                unpack4(w[i], wf);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = rstd * (g[i][j] - xh[i][j] * m);
-                if (d_sum) {
-                    float d[8];
-                    unpack8(d_sum[row * nv + c], d);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] += d[j];
+                for (int j = 0; j < 4; ++j) {
+                    dw[i][j] = fma2(g[j], mul2(xv[j], rr), dw[i][j]);
+                    g[j] = mul2(g[j], wf[j]);
+                    dot = fma2(g[j], xv[j], dot);
+                    if constexpr (KEEP) {
+                        kept_g[i][j] = g[j];
+                        kept_x[i][j] = xv[j];
+                    }
                 }
-                dx[row * nv + c] = pack8(o);
             }
         }
+        // mean(w dy xhat) rstd^2, with xhat = s rstd; the other half of s_red is free: one barrier a row
+        const float m = block_sum(dot.x + dot.y, s_red[par]) * rstd * inv_h;
+        const float2 mm = make_float2(-m * rstd * rstd, -m * rstd * rstd);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = i * NT + tid;
+            if (c < nv) {
+                float2 g[4], xv[4], o[4] = {};
+                if constexpr (KEEP) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        g[j] = kept_g[i][j];
+                        xv[j] = kept_x[i][j];
+                    }
+                } else {
+                    float2 wf[4];
+                    unpack4(*slot(st, 0, i), g);
+                    unpack4(*slot(st, 1, i), xv);
+                    unpack4(w[i], wf);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) g[j] = mul2(g[j], wf[j]);
+                }
+                if (d_sum) unpack4(*slot(st, 2, i), o);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[j] = fma2(g[j], rr, fma2(xv[j], mm, o[j]));
+                dx[row * nv + c] = pack4(o);
+            }
+        }
+        rstd = rstd_next;
+        st = st + 1 < S ? st + 1 : 0;
     }
     if (!dw_part) return;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = i * kNormThreads + threadIdx.x;
+        const int c = i * NT + tid;
         if (c < nv) {
             float4 *p = reinterpret_cast<float4 *>(dw_part + (int64_t)blockIdx.x * H + (int64_t)c * 8);
-            p[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-            p[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+            p[0] = make_float4(dw[i][0].x, dw[i][0].y, dw[i][1].x, dw[i][1].y);
+            p[1] = make_float4(dw[i][2].x, dw[i][2].y, dw[i][3].x, dw[i][3].y);
         }
     }
 }
 
-// dw[c] = sum over the blocks' partial rows, in block order (the same order every run).
-__global__ void __launch_bounds__(kNormThreads)
+// dw of 32 columns a block: 32 groups of 8 threads (4 columns each) add every 32nd partial
+// row, then the groups are added in order (the same order every run).
+__global__ void __launch_bounds__(256)
 rmsnorm_dw_kernel(const float *__restrict__ part, int blocks, int H, float *__restrict__ dw) {
     pdl_wait();
-    const int c = blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= H) return;
-    float s = 0.0f;
-    for (int b = 0; b < blocks; ++b) s += part[(int64_t)b * H + c];
-    dw[c] = s;
+    __shared__ float s_part[32][32 + 1];
+    const int q = threadIdx.x & 7, grp = threadIdx.x >> 3, c = blockIdx.x * 32 + q * 4;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < H) {
+#pragma unroll 5
+        for (int b = grp; b < blocks; b += 32) {
+            const float4 p = __ldcg(reinterpret_cast<const float4 *>(part + (int64_t)b * H + c));
+            s.x += p.x;
+            s.y += p.y;
+            s.z += p.z;
+            s.w += p.w;
+        }
+    }
+    s_part[grp][q * 4] = s.x;
+    s_part[grp][q * 4 + 1] = s.y;
+    s_part[grp][q * 4 + 2] = s.z;
+    s_part[grp][q * 4 + 3] = s.w;
+    __syncthreads();
+    if (threadIdx.x < 32 && blockIdx.x * 32 + threadIdx.x < H) {
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) t += s_part[i][threadIdx.x];
+        dw[blockIdx.x * 32 + threadIdx.x] = t;
+    }
+}
+
+// Launches KERN for rows of H columns, V vectors of 8 a thread, with `rows_smem` row slots of
+// `tensors` tensors in shared memory.
+template <auto KERN, typename... Args>
+moe_status_t launch_rows(int blocks, int H, int V, int slots, cudaStream_t s, Args &&...args) {
+    static PerDeviceOnce once;
+    int set = 0;
+    const moe_status_t st = once.get(
+        [](int *v) {
+            *v = 1;
+            return cuda_status(cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024));
+        },
+        &set);
+    if (st != MOE_OK) return st;
+    const int nt = ((H / 8 + V - 1) / V + 31) / 32 * 32;
+    const size_t smem = (size_t)slots * V * nt * sizeof(uint4);
+    if (launch_k(KERN, dim3((unsigned)blocks), dim3((unsigned)nt), smem, s, static_cast<Args &&>(args)...) !=
+        cudaSuccess) {
+        (void)cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    return launch_status();
+}
+
+template <int V, int S, typename... Args>
+moe_status_t norm_fwd(int blocks, int H, cudaStream_t s, Args &&...args) {
+    return launch_rows<add_rmsnorm_kernel<V, S>>(blocks, H, V, 2 * S, s, static_cast<Args &&>(args)...);
+}
+template <int V, int S, typename... Args>
+moe_status_t norm_bwd(int blocks, int H, cudaStream_t s, Args &&...args) {
+    return launch_rows<add_rmsnorm_bwd_kernel<V, S>>(blocks, H, V, 3 * S, s, static_cast<Args &&>(args)...);
+}
+
+// Blocks of the backward, each leaving one partial row of dw: a function of the sizes alone.
+int bwd_blocks(int64_t T, int H) {
+    const int most = kNormSms * (H <= 1024 ? 8 : H <= 2048 ? 4 : H <= 8192 ? 2 : 1);
+    return T < most ? (int)T : most;
 }
 
 moe_status_t check_norm(int64_t T, int H) {
     if (T < 0 || H < 1) return MOE_ERR_INVALID_ARG;
-    if (H % 8 != 0 || H > kNormThreads * 8 * kNormMaxVec || T > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
+    if (H % 8 != 0 || H > kNormMaxH || T > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
@@ -208,26 +393,26 @@ extern "C" moe_status_t moe_add_rmsnorm(const moe_bf16_t *x, const moe_bf16_t *r
     if (!x || !weight || (!y && !y_q)) return MOE_ERR_INVALID_ARG;
     if (!all_aligned16({x, residual, weight, sum, y}) || reinterpret_cast<uintptr_t>(y_q) % 8)
         return MOE_ERR_UNSUPPORTED;
-    const int per = (H / 8 + kNormThreads - 1) / kNormThreads;
-#define MOE_NORM(V)                                                                                               \
-    launch_k(add_rmsnorm_kernel<V>, dim3((unsigned)T), dim3(kNormThreads), 0, (cudaStream_t)stream,               \
-             reinterpret_cast<const uint4 *>(x), reinterpret_cast<const uint4 *>(residual),                       \
-             reinterpret_cast<const uint4 *>(weight), eps, H, reinterpret_cast<uint4 *>(sum),                     \
-             reinterpret_cast<uint4 *>(y), y_q, y_sf, rstd)
-    if (per <= 1) MOE_NORM(1);
-    else if (per <= 2) MOE_NORM(2);
-    else if (per <= 4) MOE_NORM(4);
-    else if (per <= 8) MOE_NORM(8);
-    else MOE_NORM(16);
+    auto u4 = [](const void *p) { return static_cast<const uint4 *>(p); };
+    auto w4 = [](void *p) { return static_cast<uint4 *>(p); };
+    // vectors a thread, rows in shared memory, blocks per SM
+#define MOE_NORM(V, S, PER_SM)                                                                                        \
+    return norm_fwd<V, S>(T < kNormSms * PER_SM ? (int)T : kNormSms * PER_SM, H, (cudaStream_t)stream, u4(x),        \
+                          u4(residual), u4(weight), eps, T, H, w4(sum), w4(y), y_q, y_sf, rstd)
+    if (H <= 1024) MOE_NORM(1, 6, 6);
+    if (H <= 2048) MOE_NORM(1, 2, 4);
+    if (H <= 4096) MOE_NORM(1, 2, 2);
+    if (H <= 8192) MOE_NORM(2, 3, 1);
+    if (H <= 16384) MOE_NORM(4, 1, 2);
+    MOE_NORM(8, 1, 1);
 #undef MOE_NORM
-    return launch_status();
 }
 
 extern "C" size_t moe_rmsnorm_bwd_workspace_bytes(int64_t T, int H) {
     using namespace moe;
     if (check_norm(T, H) != MOE_OK) return 0;
-    const int64_t blocks = T < kNormBwdBlocks ? (T > 0 ? T : 1) : kNormBwdBlocks;
-    return (size_t)blocks * (size_t)H * sizeof(float);
+    const int blocks = bwd_blocks(T, H);
+    return (size_t)(blocks > 0 ? blocks : 1) * (size_t)H * sizeof(float);
 }
 
 extern "C" moe_status_t moe_add_rmsnorm_bwd(const moe_bf16_t *dy, const moe_bf16_t *d_sum, const moe_bf16_t *sum,
@@ -243,22 +428,19 @@ extern "C" moe_status_t moe_add_rmsnorm_bwd(const moe_bf16_t *dy, const moe_bf16
     if (!all_aligned16({dy, d_sum, sum, weight, dx, dweight ? ws : nullptr})) return MOE_ERR_UNSUPPORTED;
     cudaStream_t s = (cudaStream_t)stream;
     if (T == 0) return dweight ? cuda_status(cudaMemsetAsync(dweight, 0, (size_t)H * sizeof(float), s)) : MOE_OK;
-    const int blocks = T < kNormBwdBlocks ? (int)T : kNormBwdBlocks;
+    const int blocks = bwd_blocks(T, H);
     float *part = dweight ? static_cast<float *>(ws) : nullptr;
-    const int per = (H / 8 + kNormThreads - 1) / kNormThreads;
-#define MOE_NORM_BWD(V)                                                                                           \
-    launch_k(add_rmsnorm_bwd_kernel<V>, dim3((unsigned)blocks), dim3(kNormThreads), 0, s,                         \
-             reinterpret_cast<const uint4 *>(dy), reinterpret_cast<const uint4 *>(d_sum),                         \
-             reinterpret_cast<const uint4 *>(sum), reinterpret_cast<const uint4 *>(weight), rstd, T, H,           \
-             reinterpret_cast<uint4 *>(dx), part)
-    if (per <= 1) MOE_NORM_BWD(1);
-    else if (per <= 2) MOE_NORM_BWD(2);
-    else if (per <= 4) MOE_NORM_BWD(4);
-    else if (per <= 8) MOE_NORM_BWD(8);
-    else MOE_NORM_BWD(16);
+    auto u4 = [](const void *p) { return static_cast<const uint4 *>(p); };
+#define MOE_NORM_BWD(V, S)                                                                                          \
+    norm_bwd<V, S>(blocks, H, s, u4(dy), u4(d_sum), u4(sum), u4(weight), rstd, T, H, reinterpret_cast<uint4 *>(dx), \
+                   part)
+    if (H <= 2048) st = MOE_NORM_BWD(1, 3);   // blocks per SM: bwd_blocks
+    else if (H <= 4096) st = MOE_NORM_BWD(1, 2);
+    else if (H <= 16384) st = MOE_NORM_BWD(4, 2);
+    else st = MOE_NORM_BWD(8, 1);
 #undef MOE_NORM_BWD
+    if (st != MOE_OK) return st;
     if (dweight)
-        launch_k(rmsnorm_dw_kernel, dim3((unsigned)((H + kNormThreads - 1) / kNormThreads)), dim3(kNormThreads), 0, s,
-                 part, blocks, H, dweight);
+        launch_k(rmsnorm_dw_kernel, dim3((unsigned)((H + 31) / 32)), dim3(256), 0, s, part, blocks, H, dweight);
     return launch_status();
 }
