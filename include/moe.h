@@ -672,9 +672,9 @@ MOE_API moe_status_t moe_add_rmsnorm_bwd(const moe_bf16_t *dy, const moe_bf16_t 
 
 /* moe_permute_mxfp8 for rows that are already MXFP8 (moe_add_rmsnorm's y_q / y_sf):
  *   rows_q  device uint8 [T, H] E4M3 codes; rows_sf device uint8 [T, H/32] scale bytes
- * The codes are copied and the scale bytes take the tile layout; every other argument,
- * output and limit as moe_permute_mxfp8 (rows_q and x_q 16-byte, rows_sf and x_sf 4-byte
- * aligned). */
+ * The codes are copied and the scale bytes take the tile layout (zeros in the rows of a
+ * tile past its group's end); every other argument, output and limit as moe_permute_mxfp8
+ * (rows_q, x_q and x_sf 16-byte, rows_sf 4-byte aligned). */
 MOE_API moe_status_t moe_permute_rows_mxfp8(const uint8_t *rows_q, const uint8_t *rows_sf, const int32_t *topk_idx,
                                             int64_t T, int H, int E, int k, uint8_t *x_q, uint8_t *x_sf,
                                             int64_t rows_cap, int32_t *dst_of_route, int32_t *src_of_row,
