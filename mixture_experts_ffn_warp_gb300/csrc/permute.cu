@@ -1071,6 +1071,58 @@ permute_place_kernel(const int32_t *__restrict__ topk_idx, int64_t R, int E, con
 
 constexpr int kSlab = 64;   // 128-element K blocks of a tile's scales in shared memory at a time
 
+// The scales of one 128-row tile, gathered by the whole block: s_tok[m] is the token of row m
+// (-1: none, zeros); s_sf holds SLAB 128-element K blocks of it at a time.
+template <int SLAB>
+__device__ __forceinline__ void gather_tile_scales(const uint32_t *__restrict__ rows_sf, const int *s_tok, int tile,
+                                                   int kb128, uint32_t *s_sf, uint32_t *__restrict__ x_sf) {
+    const int lane = threadIdx.x & 31;
+    for (int b0 = 0; b0 < kb128; b0 += SLAB) {
+        const int nb = kb128 - b0 < SLAB ? kb128 - b0 : SLAB;
+        for (int m = threadIdx.x >> 5; m < 128; m += kScatterWarps) {
+            const int t = s_tok[m];
+            for (int b = lane; b < nb; b += 32)
+                s_sf[m * (SLAB + 1) + b] = t >= 0 ? __ldg(rows_sf + (int64_t)t * kb128 + b0 + b) : 0u;
+        }
+        __syncthreads();
+        // 16 bytes of an atom: rows i, i + 32, i + 64, i + 96
+        for (int v = threadIdx.x; v < nb * 32; v += blockDim.x) {
+            const int b = v >> 5, i = v & 31;
+            const uint32_t *p = s_sf + i * (SLAB + 1) + b;
+            *reinterpret_cast<uint4 *>(x_sf + ((int64_t)tile * kb128 + b0 + b) * 128 + i * 4) =
+                make_uint4(p[0], p[32 * (SLAB + 1)], p[64 * (SLAB + 1)], p[96 * (SLAB + 1)]);
+        }
+        __syncthreads();
+    }
+}
+
+constexpr int kRowVecs = 16;   // 16-byte vectors of a row in a lane's registers (H <= 8192: all of it)
+
+__device__ __forceinline__ void load_row_vecs(const uint4 *__restrict__ row, int base, int vecs, uint4 (&r)[kRowVecs]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int u = 0; u < kRowVecs; ++u)
+        if (base + lane + 32 * u < vecs) r[u] = __ldcg(row + base + lane + 32 * u);
+}
+
+// A token's row to its k destinations (lane j < k holds the j-th, -1: dropped); r already
+// holds the row's first vectors.
+__device__ __forceinline__ void copy_row(const uint4 *__restrict__ row, int vecs, int k, int my_dst, uint4 (&r)[kRowVecs],
+                                         uint4 *__restrict__ x_q) {
+    const int lane = threadIdx.x & 31;
+    for (int base = 0; base < vecs; base += 32 * kRowVecs) {
+        if (base) load_row_vecs(row, base, vecs, r);
+        for (int j = 0; j < k; ++j) {
+            const int dst = __shfl_sync(0xFFFFFFFFu, my_dst, j);
+            if (dst < 0) continue;
+            uint4 *to = x_q + (int64_t)dst * vecs + base;
+#pragma unroll
+            for (int u = 0; u < kRowVecs; ++u)
+                if (base + lane + 32 * u < vecs) to[lane + 32 * u] = r[u];
+        }
+    }
+}
+
 // Blocks below scale_blocks: the scales of one 128-row tile each.  The others: the codes of
 // kScatterWarps tokens.
 __global__ void __launch_bounds__(kScatterWarps * 32)
@@ -1078,12 +1130,12 @@ permute_rows_mx_kernel(const uint4 *__restrict__ rows_q, const uint32_t *__restr
                        int H, const int32_t *__restrict__ group_offsets, const int32_t *__restrict__ mtile_start,
                        const int32_t *__restrict__ dst_of_route, const int32_t *__restrict__ src_of_row,
                        uint4 *__restrict__ x_q, uint32_t *__restrict__ x_sf, int64_t scale_blocks) {
-    __shared__ uint32_t s_sf[128 * (kSlab + 1)];
+    constexpr int SLAB = 64;
+    __shared__ uint32_t s_sf[128 * (SLAB + 1)];
     __shared__ int s_tok[128], s_group;
-    const int lane = threadIdx.x & 31;
     if ((int64_t)blockIdx.x < scale_blocks) {
         pdl_wait();
-        const int tile = blockIdx.x, kb128 = H / 128;
+        const int tile = blockIdx.x;
         if (threadIdx.x == 0) s_group = -1;
         __syncthreads();
         for (int e = threadIdx.x; e < E; e += blockDim.x)
@@ -1096,49 +1148,145 @@ permute_rows_mx_kernel(const uint4 *__restrict__ rows_q, const uint32_t *__restr
             s_tok[threadIdx.x] = row < group_offsets[e + 1] ? src_of_row[row] / k : -1;
         }
         __syncthreads();
-        for (int b0 = 0; b0 < kb128; b0 += kSlab) {
-            const int nb = kb128 - b0 < kSlab ? kb128 - b0 : kSlab;
-            for (int m = threadIdx.x >> 5; m < 128; m += kScatterWarps) {
-                const int t = s_tok[m];
-                for (int b = lane; b < nb; b += 32)
-                    s_sf[m * (kSlab + 1) + b] = t >= 0 ? __ldg(rows_sf + (int64_t)t * kb128 + b0 + b) : 0u;
-            }
-            __syncthreads();
-            // 16 bytes of an atom: rows i, i + 32, i + 64, i + 96
-            for (int v = threadIdx.x; v < nb * 32; v += blockDim.x) {
-                const int b = v >> 5, i = v & 31;
-                const uint32_t *p = s_sf + i * (kSlab + 1) + b;
-                *reinterpret_cast<uint4 *>(x_sf + ((int64_t)tile * kb128 + b0 + b) * 128 + i * 4) =
-                    make_uint4(p[0], p[32 * (kSlab + 1)], p[64 * (kSlab + 1)], p[96 * (kSlab + 1)]);
-            }
-            __syncthreads();
-        }
+        gather_tile_scales<SLAB>(rows_sf, s_tok, tile, H / 128, s_sf, x_sf);
         return;
     }
+    const int lane = threadIdx.x & 31, vecs = H / 16;
     const int64_t t = ((int64_t)blockIdx.x - scale_blocks) * kScatterWarps + (threadIdx.x >> 5);
-    const int vecs = H / 16;
-    constexpr int U = 16;   // 16-byte vectors of the row in a lane's registers (H <= 8192: all of it)
-    uint4 r[U];
-    auto load = [&](int base) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t < T && base + lane + 32 * u < vecs) r[u] = __ldcg(rows_q + t * vecs + base + lane + 32 * u);
-    };
-    load(0);   // written before the counting pass ran: need not wait for it
+    uint4 r[kRowVecs];
+    if (t < T) load_row_vecs(rows_q + t * vecs, 0, vecs, r);   // complete before the counting pass ran: no need to wait
     pdl_wait();
     if (t >= T) return;
-    const int my_dst = lane < k ? dst_of_route[t * k + lane] : -1;
-    for (int base = 0; base < vecs; base += 32 * U) {
-        if (base) load(base);
-        for (int j = 0; j < k; ++j) {
-            const int dst = __shfl_sync(0xFFFFFFFFu, my_dst, j);
-            if (dst < 0) continue;
-            uint4 *to = x_q + (int64_t)dst * vecs + base;
+    copy_row(rows_q + t * vecs, vecs, k, lane < k ? dst_of_route[t * k + lane] : -1, r, x_q);
+}
+
+// Up to kSmallRoutes routes: one kernel.  Every block ranks all the routes for itself in shared
+// memory (about 2 us) instead of waiting for a counting pass, then does its share of
+// the codes or scales; block 0 writes the maps.  600 routes of 2048: 9.3 us in two launches.
+constexpr int kSmallRoutes = 2048;
+
+size_t small_smem(int64_t R, int E) { return (size_t)(2 * (E + 1)) * 4 + (size_t)(kScatterWarps * E + 2 * R) * 2; }
+
+__global__ void __launch_bounds__(kScatterWarps * 32)
+permute_rows_small_kernel(const uint4 *__restrict__ rows_q, const uint32_t *__restrict__ rows_sf,
+                          const int32_t *__restrict__ topk_idx, int T, int k, int E, int H,
+                          int32_t *__restrict__ dst_of_route, int32_t *__restrict__ src_of_row,
+                          int32_t *__restrict__ group_sizes, int32_t *__restrict__ group_offsets,
+                          uint4 *__restrict__ x_q, uint32_t *__restrict__ x_sf, int scale_blocks, uint32_t *err) {
+    constexpr int SLAB = 24;   // with the largest maps within 48 KB
+    extern __shared__ int32_t s_off[];                                   // [E + 1] first row of each group
+    int32_t *s_mt = s_off + E + 1;                                       // [E + 1] its first 128-row tile
+    uint16_t *s_cnt = reinterpret_cast<uint16_t *>(s_mt + E + 1);        // [kScatterWarps][E]
+    uint16_t *s_row = s_cnt + kScatterWarps * E;                         // [R] row of each route, 0xFFFF: dropped
+    uint16_t *s_src = s_row + T * k;                                     // [R] route of each row
+    __shared__ uint32_t s_sf[128 * (SLAB + 1)];
+    __shared__ int s_tok[128], s_group, s_wsum[kScatterWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = T * k;
+    for (int i = tid; i < kScatterWarps * E; i += blockDim.x) s_cnt[i] = 0;
+    if (tid == 0) s_group = -1;
+    __syncthreads();
+    pdl_wait();
+
+    // ranks among the routes of the warp's share, in route order
+    const int per = ((R + kScatterWarps - 1) / kScatterWarps + 31) / 32 * 32;
+    uint16_t *cnt = s_cnt + warp * E;
+    for (int i = 0; i < per; i += 32) {
+        const int r = warp * per + i + lane;
+        int e = r < R ? topk_idx[r] : -1;
+        if (e < -1 || e >= E) {
+            if (blockIdx.x == 0) raise_device_error(err, MOE_DEVERR_BAD_EXPERT_ID);
+            e = -1;
+        }
+        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, e);
+        const int before = __popc(peers & ((1u << lane) - 1));
+        if (e >= 0) s_row[r] = (uint16_t)(cnt[e] + before);
+        __syncwarp();
+        if (e >= 0 && before == 0) cnt[e] = (uint16_t)(cnt[e] + __popc(peers));
+        __syncwarp();
+    }
+    __syncthreads();
+    // group sizes; offsets and tiles by a scan over the experts, 4 a thread (both sums in one word)
+    int own[4], sum = 0;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (base + lane + 32 * u < vecs) to[lane + 32 * u] = r[u];
+    for (int i = 0; i < 4; ++i) {
+        const int e = tid * 4 + i;
+        own[i] = 0;
+        if (e < E) {
+            int run = 0;
+            for (int w = 0; w < kScatterWarps; ++w) {
+                const int c = s_cnt[w * E + e];
+                s_cnt[w * E + e] = (uint16_t)run;
+                run += c;
+            }
+            own[i] = (run << 16) | ((run + 127) / 128);
+            if (blockIdx.x == 0) group_sizes[e] = run;
+        }
+        sum += own[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+        if (lane >= off) incl += o;
+    }
+    if (lane == 31) s_wsum[warp] = incl;
+    __syncthreads();
+    int excl = incl - sum;
+    for (int w = 0; w < warp; ++w) excl += s_wsum[w];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = tid * 4 + i;
+        if (e < E) {
+            s_off[e] = excl >> 16;
+            s_mt[e] = excl & 0xFFFF;
+            excl += own[i];
+            if (e == E - 1) {
+                s_off[E] = excl >> 16;
+                s_mt[E] = excl & 0xFFFF;
+            }
         }
     }
+    __syncthreads();
+    for (int i = 0; i < per; i += 32) {
+        const int r = warp * per + i + lane;
+        if (r >= R) break;
+        const int e = topk_idx[r];
+        int row = -1;
+        if (e >= 0 && e < E) {
+            row = s_off[e] + cnt[e] + s_row[r];
+            s_src[row] = (uint16_t)r;
+        }
+        s_row[r] = (uint16_t)row;
+        if (blockIdx.x == 0) {
+            dst_of_route[r] = row;
+            if (row >= 0) src_of_row[row] = r;
+        }
+    }
+    if (blockIdx.x == 0)
+        for (int e = tid; e <= E; e += blockDim.x) group_offsets[e] = s_off[e];
+    __syncthreads();
+
+    if ((int)blockIdx.x < scale_blocks) {
+        const int tile = blockIdx.x;
+        for (int e = tid; e < E; e += blockDim.x)
+            if (s_mt[e] <= tile && tile < s_mt[e + 1]) s_group = e;
+        __syncthreads();
+        const int e = s_group;
+        if (e < 0) return;   // past the last tile
+        if (tid < 128) {
+            const int row = s_off[e] + (tile - s_mt[e]) * 128 + tid;
+            s_tok[tid] = row < s_off[e + 1] ? s_src[row] / k : -1;
+        }
+        __syncthreads();
+        gather_tile_scales<SLAB>(rows_sf, s_tok, tile, H / 128, s_sf, x_sf);
+        return;
+    }
+    const int t = ((int)blockIdx.x - scale_blocks) * kScatterWarps + warp, vecs = H / 16;
+    if (t >= T) return;
+    uint4 r[kRowVecs];
+    load_row_vecs(rows_q + (int64_t)t * vecs, 0, vecs, r);
+    const int row = lane < k ? s_row[t * k + lane] : 0xFFFF;
+    copy_row(rows_q + (int64_t)t * vecs, vecs, k, row == 0xFFFF ? -1 : row, r, x_q);
 }
 
 }  // namespace
@@ -1168,6 +1316,15 @@ extern "C" moe_status_t moe_permute_rows_mxfp8(const uint8_t *rows_q, const uint
     const int64_t chunks = perm_chunks(R);
     int32_t *counts = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + kWsHeaderBytes);
     int32_t *mtile = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + kWsHeaderBytes + ws_counts_bytes(chunks, E));
+    const int64_t scale_blocks = R / 128 + (R < E ? R : E);   // at least the tiles of any routing
+    const unsigned blocks = (unsigned)(scale_blocks + (T + kScatterWarps - 1) / kScatterWarps);
+    if (R > 0 && R <= kSmallRoutes) {
+        launch_k(permute_rows_small_kernel, dim3(blocks), dim3(kScatterWarps * 32), small_smem(R, E), s,
+                 reinterpret_cast<const uint4 *>(rows_q), reinterpret_cast<const uint32_t *>(rows_sf), topk_idx, (int)T,
+                 k, E, H, dst_of_route, src_of_row, group_sizes, group_offsets, reinterpret_cast<uint4 *>(x_q),
+                 reinterpret_cast<uint32_t *>(x_sf), (int)scale_blocks, err);
+        return launch_status();
+    }
     bool final_rows = false;
     if (count_and_scan(topk_idx, R, E, 1, rows_cap, dst_of_route, src_of_row, counts, group_sizes, group_offsets, mtile,
                        ws_done_counter(ws), err, s, &final_rows) != MOE_OK)
@@ -1176,9 +1333,7 @@ extern "C" moe_status_t moe_permute_rows_mxfp8(const uint8_t *rows_q, const uint
     if (!final_rows)
         launch_k(permute_place_kernel, dim3((unsigned)((R + 255) / 256)), dim3(256), 0, s, topk_idx, R, E, counts,
                  dst_of_route, src_of_row, rows_cap, err);
-    const int64_t scale_blocks = R / 128 + (R < E ? R : E);   // at least the tiles of any routing
-    launch_k(permute_rows_mx_kernel, dim3((unsigned)(scale_blocks + (T + kScatterWarps - 1) / kScatterWarps)),
-             dim3(kScatterWarps * 32), 0, s, reinterpret_cast<const uint4 *>(rows_q),
+    launch_k(permute_rows_mx_kernel, dim3(blocks), dim3(kScatterWarps * 32), 0, s, reinterpret_cast<const uint4 *>(rows_q),
              reinterpret_cast<const uint32_t *>(rows_sf), T, k, E, H, group_offsets, mtile, dst_of_route, src_of_row,
              reinterpret_cast<uint4 *>(x_q), reinterpret_cast<uint32_t *>(x_sf), scale_blocks);
     return launch_status();

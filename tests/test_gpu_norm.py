@@ -229,7 +229,8 @@ def test_other_stream():
 # ------------------------------------------------------------------ quantised rows to the experts
 
 @pytest.mark.parametrize("T,H,E,k", [(1, 128, 4, 1), (1, 7168, 256, 8), (100, 2048, 64, 6), (257, 384, 8, 2),
-                                     (3000, 256, 5, 3), (70, 128, 40, 32), (5000, 512, 128, 8)])
+                                     (3000, 256, 5, 3), (70, 128, 40, 32), (5000, 512, 128, 8),
+                                     (64, 3200, 1024, 32), (1000, 9216, 3, 2), (16, 128, 1, 1)])
 def test_permute_rows_equals_quantising_permute(T, H, E, k):
     """Rows quantised first and permuted after = quantised by the permutation, bit for bit."""
     rows, _, _ = inputs(T, H, seed=T + E, residual=False)
