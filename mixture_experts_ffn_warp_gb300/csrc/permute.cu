@@ -1081,9 +1081,18 @@ __device__ __forceinline__ void gather_tile_scales(const uint32_t *__restrict__ 
         const int nb = kb128 - b0 < SLAB ? kb128 - b0 : SLAB;
         for (int m = threadIdx.x >> 5; m < 128; m += kScatterWarps) {
             const int t = s_tok[m];
-            for (int b = lane; b < nb; b += 32)
-                s_sf[m * (SLAB + 1) + b] = t >= 0 ? __ldg(rows_sf + (int64_t)t * kb128 + b0 + b) : 0u;
+            for (int b = lane; b < nb; b += 32) {
+                uint32_t *to = s_sf + m * (SLAB + 1) + b;
+                if (t >= 0)   // all of the slab's words in flight at once
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                                     static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+                                 "l"(rows_sf + (int64_t)t * kb128 + b0 + b)
+                                 : "memory");
+                else
+                    *to = 0u;
+            }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
         // 16 bytes of an atom: rows i, i + 32, i + 64, i + 96
         for (int v = threadIdx.x; v < nb * 32; v += blockDim.x) {
