@@ -49,6 +49,7 @@ namespace {
 constexpr int kDecWarps = 12;        // weights, x / h, MMA, idle, 4 drain, 4 join
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kRouteWarps = kDecWarps - 1;   // all but the one that sets up
+constexpr int kRouteAlone = 16;              // tokens up to which every CTA routes for itself
 constexpr int kDecMaxStages = 8;
 constexpr int kDecMaxCtas = 160;
 constexpr int kDecMaxExperts = 1024;
@@ -62,6 +63,7 @@ constexpr uint32_t kDecSmemMax = 232448;
 struct CounterSet {
     uint32_t queue;                  // segments drawn beyond each CTA's first
     uint32_t x_ready;                // CTAs whose share of x is quantised (MXFP8)
+    uint32_t routed;                 // tokens routed (more than kRouteAlone tokens)
     uint32_t finished;               // CTAs whose roles have ended
     uint32_t down_done;              // down segments whose partial sums are written
     uint32_t up_done[kDecMaxExperts];   // gate / up segments of the i-th expert hit
@@ -74,17 +76,20 @@ struct Counters {
 constexpr size_t kDecCtrBytes = (sizeof(Counters) + 1023) / 1024 * 1024;
 
 // Pieces that the K range of a tile is cut into: a rule on the sizes and the number of experts
-// hit, so that the order of the sums is the same wherever the call runs.  About 8 segments per
-// CTA; the down segments of the last `tail` experts, whose end is the call's end, are four times
-// finer, and `tail` is large enough for every CTA to spend one of the long segments on them.
-// More tokens make a segment's partial sums larger: the shortest piece grows with them.
+// hit, so that the order of the sums is the same wherever the call runs.  About 5 segments per
+// CTA, none shorter than `lo` chunks; the down segments of the last `tail` experts, whose end is
+// the call's end, are up to four times finer, and `tail` is large enough for every CTA to
+// spend one of the long segments on them.  More tokens make a segment's partial sums
+// larger: the shortest piece grows with them.  With 8 segments per CTA and pieces from one chunk up:
+// 37 tokens fine_grained on MXFP8 106 us (92), one token of them 30 us (25), 64 tokens of bf16
+// 179 us (172); with 4 segments per CTA or 12 nothing gained.
 struct Pieces {
     int up, down, last, tail;
 };
 __host__ __device__ inline Pieces pieces_of(int A, int FT, int NT, int K1, int K2, int T) {
     const int64_t per_cta = (int64_t)A * ((int64_t)FT * K1 + (int64_t)NT * K2) / kDecMaxCtas;
-    const int lo = 1 + T / 16;
-    const int64_t c = per_cta / 8, f = per_cta / 32;
+    const int lo = 4 + T / 16;
+    const int64_t c = per_cta / 5, f = per_cta / 20;
     const int p = (int)(c < lo ? lo : c > 64 ? 64 : c), l = (int)(f < lo ? lo : f > 8 ? 8 : f);
     const int tail = (int)(((int64_t)p * kDecMaxCtas + (int64_t)NT * K2 - 1) / ((int64_t)NT * K2));
     return Pieces{(K1 + p - 1) / p, (K2 + p - 1) / p, (K2 + l - 1) / l, tail < A ? tail : A};
@@ -106,6 +111,7 @@ struct DecArgs {
     uint8_t *hq;                     // h as blocks of the MMA operand
     float *part1;                    // partial sums [route][F / 128][piece][256]: gate, up
     float *part2;                    // partial sums [route][H / 256][piece][256]
+    int room1, room2;                // pieces that part1 and part2 have room for
     int stages;
     uint32_t stage_bytes;
     uint32_t off_meta;               // shared memory behind the ring
@@ -251,11 +257,11 @@ struct Seg {
     int r0;            // routes of the experts before it
 };
 
-// Top-k routing of tokens w, w + kRouteWarps, ... into shared memory: each lane holds experts
-// lane, lane + 32, ... (V of them) in registers.  `meanwhile` runs while the first token's
+// Top-k routing of tokens t0, t0 + step, ... by a warp: each lane holds experts lane,
+// lane + 32, ... (V of them) in registers.  `meanwhile` runs while the first token's
 // logits are on their way.
 template <int V, typename F>
-__device__ __forceinline__ void route_tokens(const DecArgs &a, int w, int lane, bool write, uint32_t *s_mask,
+__device__ __forceinline__ void route_tokens(const DecArgs &a, int t0, int step, int lane, bool write, uint32_t *s_mask,
                                              uint16_t *s_idx, float *s_w, F &&meanwhile) {
     float next[V], bias[V];
     auto load = [&](int t) {
@@ -263,13 +269,13 @@ __device__ __forceinline__ void route_tokens(const DecArgs &a, int w, int lane, 
         for (int i = 0; i < V; ++i)
             next[i] = lane + 32 * i < a.E ? __ldg(a.logits + (int64_t)t * a.E + lane + 32 * i) : 0.0f;
     };
-    if (w < a.T) load(w);
+    if (t0 < a.T) load(t0);
     if (a.sigmoid) {
 #pragma unroll
         for (int i = 0; i < V; ++i) bias[i] = a.bias && lane + 32 * i < a.E ? __ldg(a.bias + lane + 32 * i) : 0.0f;
     }
     meanwhile();
-    for (int t = w; t < a.T; t += kRouteWarps) {
+    for (int t = t0; t < a.T; t += step) {
         uint32_t key[V];
         float score[V];                                // sigmoid: the unbiased score
 #pragma unroll
@@ -281,7 +287,7 @@ __device__ __forceinline__ void route_tokens(const DecArgs &a, int w, int lane, 
             }
             key[i] = lane + 32 * i < a.E ? order_key(r) : 0u;
         }
-        if (t + kRouteWarps < a.T) load(t + kRouteWarps);
+        if (t + step < a.T) load(t + step);
         int mine = 0;                                  // lane j keeps slot j: the expert, its logit or score
         float val = 0.0f;
         for (int j = 0; j < a.k; ++j) {
@@ -332,6 +338,13 @@ __device__ __forceinline__ void route_tokens(const DecArgs &a, int w, int lane, 
     }
 }
 
+// More than 256 experts: 32 a lane.  Kept out of the kernel's body, whose registers it would spill
+// (0.7 us of a small call).
+__device__ __noinline__ void route_tokens_wide(const DecArgs &a, int t0, int step, int lane, bool write,
+                                               uint32_t *s_mask, uint16_t *s_idx, float *s_w) {
+    route_tokens<32>(a, t0, step, lane, write, s_mask, s_idx, s_w, []() {});
+}
+
 template <bool MX>
 __global__ void __launch_bounds__(kDecThreads, 1)
 decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmG,
@@ -365,9 +378,12 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     // ------------------------------------------------------------ set-up and routing
     const uint32_t epoch = __ldcg(&a.ctr->epoch);
     CounterSet *ctr = &a.ctr->set[epoch & 1];
-    // Warp 3, which has no role, sets up barriers and TMEM; the others route, every CTA for
-    // itself.  Meanwhile (MXFP8): this CTA's share of x, blocks of 32 elements, a warp each,
-    // into [H / 128] blocks of 2 T16 operand rows (first terms, then second) and a scale atom.
+    // Warp 3, which has no role, sets up barriers and TMEM; the others route.  Up to kRouteAlone
+    // tokens every CTA routes for itself; more are shared out, a token a CTA, and read back
+    // from topk_idx / topk_w (64 tokens of 128 experts: the routing took 10 us alone, 4 us shared).
+    // Meanwhile (MXFP8): this CTA's share of x, blocks of 32 elements, a warp each, into
+    // [H / 128] blocks of 2 T16 operand rows (first terms, then second) and a scale atom.
+    const bool alone = a.T <= kRouteAlone;
     if (warp == 3) {
         if (lane == 0) {
             for (int s = 0; s < a.stages; ++s) {
@@ -421,10 +437,33 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
             if (MX && threadIdx.x == 0) count_release(&ctr->x_ready, 1);
         };
         uint32_t *mask32 = reinterpret_cast<uint32_t *>(s_mask);
-        if (a.E <= 64) route_tokens<2>(a, rw, lane, cta == 0, mask32, s_idx, s_w, meanwhile);
-        else if (a.E <= 128) route_tokens<4>(a, rw, lane, cta == 0, mask32, s_idx, s_w, meanwhile);
-        else if (a.E <= 256) route_tokens<8>(a, rw, lane, cta == 0, mask32, s_idx, s_w, meanwhile);
-        else route_tokens<32>(a, rw, lane, cta == 0, mask32, s_idx, s_w, meanwhile);
+        const int t0 = alone ? rw : rw == 0 ? cta : a.T, step = alone ? kRouteWarps : G;
+        const bool write = !alone || cta == 0;
+        if (a.E <= 64) route_tokens<2>(a, t0, step, lane, write, mask32, s_idx, s_w, meanwhile);
+        else if (a.E <= 128) route_tokens<4>(a, t0, step, lane, write, mask32, s_idx, s_w, meanwhile);
+        else if (a.E <= 256) route_tokens<8>(a, t0, step, lane, write, mask32, s_idx, s_w, meanwhile);
+        else {
+            meanwhile();
+            route_tokens_wide(a, t0, step, lane, write, mask32, s_idx, s_w);
+        }
+        if (!alone) {
+            if (rw == 0) {
+                __syncwarp();
+                int n = 0;
+                for (int t = cta; t < a.T; t += G) ++n;
+                if (lane == 0) {
+                    if (n) count_release(&ctr->routed, (uint32_t)n);
+                    wait_count(&ctr->routed, (uint32_t)a.T, abort, a.err, limit);
+                }
+            }
+            asm volatile("barrier.cta.sync 3, %0;" ::"n"(kRouteWarps * 32) : "memory");
+            for (int i = rw * 32 + lane; i < R; i += kRouteWarps * 32) {
+                const int e = min(max(__ldcg(a.topk_idx + i), 0), a.E - 1), t = i / a.k;   // (in range, after a timeout too)
+                s_idx[i] = (uint16_t)e;
+                s_w[i] = __ldcg(a.topk_w + i);
+                atomicOr(&mask32[2 * e + (t >> 5)], 1u << (t & 31));
+            }
+        }
     }
     sm100::tc_fence_before();
     __syncthreads();
@@ -470,14 +509,41 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
 
     const uint32_t tmem = s_tmem;
     const int FT = a.F / 128, K1 = a.H / KC, K2 = a.F / KC, NT = (a.H + 255) / 256;
-    const Pieces pc = pieces_of(A, FT, NT, K1, K2, a.T);
-    const int S2 = pc.down > pc.last ? pc.down : pc.last;   // pieces that part2 has room for
+    Pieces pc = pieces_of(A, FT, NT, K1, K2, a.T);
+    pc.up = min(pc.up, a.room1);
+    pc.down = min(pc.down, a.room2);
+    pc.last = min(pc.last, a.room2);
+    const int S2 = a.room2;
     const int head = A - pc.tail;                          // experts whose down segments are the long ones
     const int n_up = A * FT * pc.up, n_down = head * NT * pc.down + pc.tail * NT * pc.last;
     const uint32_t row_bytes = MX ? 2u * a.F : 4u * a.F;    // bytes of h per padded row, both terms
     auto h_block = [&](int ai, int c16, int kc) {           // block kc of the expert's h
         const uint32_t bytes = (uint32_t)c16 * 256 + (MX ? kSfBytes : 0);
         return a.hq + (size_t)s_row0[ai] * row_bytes + (MX ? (size_t)ai * FT * kSfBytes : 0) + (size_t)kc * bytes;
+    };
+
+    // h of route r0 + i (the expert's i-th token), feature 128 ft + col, col = 32 (warp % 4) + lane:
+    // the first term's row is i, the second's c16 + i
+    auto store_h = [&](int ai, int c16, int ft, int i, float v) {
+        const int q = warp & 3, col = q * 32 + lane;
+        if constexpr (MX) {
+            uint8_t code[2], sf[2];
+            two_terms(v, code, sf);
+            uint8_t *blk = h_block(ai, c16, ft);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const uint32_t row = i + m * c16;
+                blk[sw128(row, col)] = code[m];
+                if (lane == 0) blk[c16 * 256 + sf_byte(row, q)] = sf[m];
+            }
+        } else {
+            const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+            const float hf = __bfloat162float(hi);
+            const __nv_bfloat16 lo = __float2bfloat16_rn(isinf(hf) ? 0.0f : v - hf);
+            uint8_t *blk = h_block(ai, c16, 2 * ft + col / 64);
+            *reinterpret_cast<__nv_bfloat16 *>(blk + sw128(i, (col % 64) * 2)) = hi;
+            *reinterpret_cast<__nv_bfloat16 *>(blk + sw128(i + c16, (col % 64) * 2)) = lo;
+        }
     };
 
     if (warp == 0) {
@@ -705,11 +771,28 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
             // down: column = token's index in the expert, the second term's c16 further
             const uint32_t second = s.down ? s.c16 : a.T16;
             const bool terms = MX || s.down;
+            const bool direct = !s.down && pc.up == 1;     // the whole K range: h without partial sums
             float *part = s.down ? a.part2 + (((size_t)s.r0 * NT + s.tile) * S2 + s.piece) * 256 + col
                                  : a.part1 + (((size_t)s.r0 * FT + s.tile) * pc.up + s.piece) * 256 + col;
             const size_t step = (size_t)(s.down ? NT * S2 : FT * pc.up) * 256;
             uint64_t m = s_mask[s.e];
-            for (int i0 = 0; i0 < s.cnt; i0 += 8) {
+#pragma unroll 1
+            for (int i = 0; direct && i < s.cnt; ++i) {
+                const uint32_t c = __ffsll((long long)m) - 1;
+                m &= m - 1;
+                uint32_t y[8] = {};
+                tmem_ld1(d0 + c, y[0]);
+                tmem_ld1(d1 + c, y[1]);
+                if (terms) {
+                    tmem_ld1(d0 + second + c, y[2]);
+                    tmem_ld1(d1 + second + c, y[3]);
+                }
+                tmem_ld_wait8(y);
+                store_h(s.ai, s.c16, s.tile, i,
+                        swiglu(__uint_as_float(y[0]) + __uint_as_float(y[2]),
+                               __uint_as_float(y[1]) + __uint_as_float(y[3]), a));
+            }
+            for (int i0 = 0; !direct && i0 < s.cnt; i0 += 8) {
                 uint32_t y0[8] = {}, y1[8] = {}, z0[8] = {}, z1[8] = {};
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -738,8 +821,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
             sm100::tc_fence_before();
             sm100::mbar_arrive(&tempty[buf]);
             if (++buf == a.nbuf) { buf = 0; acc_phase ^= 1u; }
+            if (direct) fence_proxy_async_global();        // h is read next by bulk copies
             all_of_four<1>(true);
-            if (threadIdx.x == 128) count_release(s.down ? &ctr->down_done : &ctr->up_done[s.ai], 1);
+            if (threadIdx.x == 128)
+                count_release(s.down ? &ctr->down_done : direct ? &ctr->h_done[s.ai] : &ctr->up_done[s.ai],
+                              direct ? s.cnt : 1);
         }
     } else if (warp >= 8) {
         // ======================================================== join: partial sums -> h
@@ -749,7 +835,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
             uint32_t *z = reinterpret_cast<uint32_t *>(&a.ctr->set[(epoch & 1) ^ 1]);
             for (int i = threadIdx.x - 256; i < (int)(sizeof(CounterSet) / 4); i += 128) z[i] = 0;
         }
-        for (int ai = 0; ai < A; ++ai) {
+        for (int ai = 0; pc.up > 1 && ai < A; ++ai) {
             // items (route, 128 features) of the expert; item id belongs to CTA id % G
             const int r0 = s_r0[ai], cnt = __popcll(s_mask[s_active[ai]]), c16 = (cnt + 15) & ~15;
             const int end = (r0 + cnt) * FT;
@@ -770,24 +856,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
                     u += __ldcg(p + j * 256 + 128);
                 }
                 const float v = swiglu(g, u, a);
-                if constexpr (MX) {
-                    uint8_t code[2], sf[2];
-                    two_terms(v, code, sf);
-                    uint8_t *blk = h_block(ai, c16, ft);
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        const uint32_t row = i + m * c16;
-                        blk[sw128(row, col)] = code[m];
-                        if (lane == 0) blk[c16 * 256 + sf_byte(row, warp - 8)] = sf[m];
-                    }
-                } else {
-                    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-                    const float hf = __bfloat162float(hi);
-                    const __nv_bfloat16 lo = __float2bfloat16_rn(isinf(hf) ? 0.0f : v - hf);
-                    uint8_t *blk = h_block(ai, c16, 2 * ft + col / 64);
-                    *reinterpret_cast<__nv_bfloat16 *>(blk + sw128(i, (col % 64) * 2)) = hi;
-                    *reinterpret_cast<__nv_bfloat16 *>(blk + sw128(i + c16, (col % 64) * 2)) = lo;
-                }
+                store_h(ai, c16, ft, i, v);
             }
             fence_proxy_async_global();   // read next by bulk copies
             all_of_four<2>(true);
@@ -867,6 +936,7 @@ struct Clamp {
 
 struct DecLayout {
     size_t xq, hq, part1, part2, total;
+    int room1, room2;   // pieces
 };
 
 size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
@@ -890,6 +960,8 @@ DecLayout decode_layout(int64_t T, int H, int F, int E, int k) {
         n1 = (size_t)p.up > n1 ? p.up : n1;
         n2 = down > n2 ? down : n2;
     }
+    l.room1 = (int)n1;
+    l.room2 = (int)n2;
     l.part2 = l.part1 + R * FT * n1 * 1024;
     l.total = l.part2 + R * NT * n2 * 1024;
     return l;
@@ -931,6 +1003,8 @@ moe_status_t launch_decode(DecArgs a, const moe_bf16_t *const (&W)[3], void *ws,
     a.hq = reinterpret_cast<uint8_t *>(base + l.hq);
     a.part1 = reinterpret_cast<float *>(base + l.part1);
     a.part2 = reinterpret_cast<float *>(base + l.part2);
+    a.room1 = l.room1;
+    a.room2 = l.room2;
 
     const int R = a.T * a.k, act = R < a.E ? R : a.E;
     const uint32_t b_bytes = (uint32_t)a.T16 * 256 + (MX ? 3 * kSfBytes : 0);   // x or h, all scale atoms
