@@ -384,6 +384,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     // Meanwhile (MXFP8): this CTA's share of x, blocks of 32 elements, a warp each, into
     // [H / 128] blocks of 2 T16 operand rows (first terms, then second) and a scale atom.
     const bool alone = a.T <= kRouteAlone;
+    int late = 0;                                      // a wait for the other CTAs' routing that gave up
     if (warp == 3) {
         if (lane == 0) {
             for (int s = 0; s < a.stages; ++s) {
@@ -453,7 +454,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
                 for (int t = cta; t < a.T; t += G) ++n;
                 if (lane == 0) {
                     if (n) count_release(&ctr->routed, (uint32_t)n);
-                    wait_count(&ctr->routed, (uint32_t)a.T, abort, a.err, limit);
+                    wait_count(&ctr->routed, (uint32_t)a.T, &late, a.err, limit);
                 }
             }
             asm volatile("barrier.cta.sync 3, %0;" ::"n"(kRouteWarps * 32) : "memory");
@@ -468,6 +469,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     sm100::tc_fence_before();
     __syncthreads();
     sm100::tc_fence_after();
+    if (late) s_abort = 1;
     // The experts that are hit, ascending, with the routes and the 16-row blocks of h before each:
     // 32 experts a warp, their totals first.  (Routes and padded rows are summed in one word:
     // 64 tokens * 32 experts keep each half below 2^16 within a chunk.)

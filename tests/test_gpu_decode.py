@@ -12,7 +12,7 @@ import torch
 
 from helpers import assert_close_rms
 from mixture_experts_ffn_warp_gb300 import (DecodeWorkspace, MoeDecode, MoeDecodeMX, MoeForward, MxWeights, moe_decode,
-                                            moe_route_topk, moe_route_topk_sigmoid)
+                                            moe_dequantize_weights_mxfp8, moe_route_topk, moe_route_topk_sigmoid)
 from mixture_experts_ffn_warp_gb300._binding import DEVERR_TIMEOUT, MoeError
 
 pytestmark = pytest.mark.gpu
@@ -257,11 +257,12 @@ def test_refusals():
         MoeDecode(T, H, F, E, k, router="hash")
 
 
+@pytest.mark.parametrize("T", [4, 40])
 @pytest.mark.parametrize("mx", [False, True])
-def test_wait_timeout_then_recovery(mx):
+def test_wait_timeout_then_recovery(mx, T):
     """With the device waits limited to 1 ns the call reports the timeout instead of finishing; after the
     workspace is initialised again the same call is right (no trap, no hang, nothing left allocated)."""
-    T, H, F, E, k = 4, 512, 512, 8, 2
+    H, F, E, k = 512, 512, 8, 2
     x, lg, W = make(T, H, F, E, seed=10)
     mw = MxWeights(*W) if mx else None
     m = (MoeDecodeMX if mx else MoeDecode)(T, H, F, E, k)
@@ -274,3 +275,28 @@ def test_wait_timeout_then_recovery(mx):
     assert m.ws.read_error() == 0
     idx, w = moe_route_topk(lg, k)
     check(out, reference(x, mw.dequantized() if mx else W, idx, w), mx)
+
+
+def test_offsets_past_32_bits():
+    """Expert weights of more than 2^31 elements a matrix: the last experts are read right."""
+    T, H, F, E, k = 3, 7168, 2048, 256, 4
+    assert E * H * F > 2 ** 31
+    g = gen(11)
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    lg = torch.randn(T, E, generator=g, device="cuda")
+    lg[:, -6:] += 20.0
+    W = [torch.empty(E, a, b, dtype=torch.bfloat16, device="cuda") for a, b in ((H, F), (H, F), (F, H))]
+    for w in W:
+        for e in range(E):
+            w[e] = torch.randn(w.shape[1:], generator=g, device="cuda", dtype=torch.bfloat16) * 0.02
+    idx, w = moe_route_topk(lg, k)
+    assert int(idx.min()) >= E - 6
+    out = MoeDecode(T, H, F, E, k)(x, lg, *W)
+    check(out, reference(x, W, idx, w))
+    mw = MxWeights(*W)
+    for i, (q, sf, K, N) in enumerate(((mw.Wg_q, mw.Wg_sf, H, F), (mw.Wu_q, mw.Wu_sf, H, F), (mw.Wd_q, mw.Wd_sf, F, H))):
+        n = K * N
+        for e in idx.unique().tolist():             # the values of the hit experts' codes
+            W[i][e] = moe_dequantize_weights_mxfp8(q[e * n:(e + 1) * n], sf[e * n // 32:(e + 1) * n // 32], 1, K, N)[0]
+    out = MoeDecodeMX(T, H, F, E, k)(x, lg, mw)
+    check(out, reference(x, W, idx, w), mx=True)

@@ -226,6 +226,25 @@ def test_other_stream():
     assert torch.equal(got.y, want.y)
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows are read and written where they belong."""
+    T, H = 530000, 4096
+    assert T * H > 2 ** 31
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    rows = [0, 1, T // 2, T - 2, T - 1]
+    few, r, w = inputs(len(rows), H, seed=12)
+    x[rows] = few
+    o = moe_add_rmsnorm(x, w, EPS, mxfp8=True)
+    want = moe_add_rmsnorm(few, w, EPS, mxfp8=True)
+    for n in ("y", "y_q", "y_sf", "rstd"):
+        assert torch.equal(getattr(o, n)[rows], getattr(want, n)), n
+    assert (o.y[2:T // 2] == 0).all()
+    dx, dw = moe_add_rmsnorm_bwd(o.y, x, w, o.rstd)
+    want_dx, want_dw = moe_add_rmsnorm_bwd(want.y, few, w, want.rstd)
+    assert torch.equal(dx[rows], want_dx)
+    torch.testing.assert_close(dw, want_dw, rtol=1e-5, atol=1e-5)   # (the zero rows add nothing; another order)
+
+
 # ------------------------------------------------------------------ quantised rows to the experts
 
 @pytest.mark.parametrize("T,H,E,k", [(1, 128, 4, 1), (1, 7168, 256, 8), (100, 2048, 64, 6), (257, 384, 8, 2),
