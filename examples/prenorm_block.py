@@ -1,0 +1,97 @@
+"""A pre-norm MoE block around this package's operators, as a model would run it.
+
+    python examples/prenorm_block.py
+
+  generation  residual add + RMS norm -> router -> MoeDecode (or MoeDecodeMX): a few tokens
+  prompt      residual add + RMS norm to bf16 (for the router) and MXFP8 (for the experts) ->
+              MoeForwardMX on the quantised rows
+  training    residual add + RMS norm -> router -> MoeForward, and back: MoeBackward, the norm's
+              backward
+
+The router's projection is the model's own (a plain product here)."""
+from __future__ import annotations
+
+import os
+import sys
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+from mixture_experts_ffn_warp_gb300 import (MoeBackward, MoeDecode, MoeDecodeMX, MoeForward, MoeForwardMX,  # noqa: E402
+                                            MxWeights, NormOutput, NormWorkspace, moe_add_rmsnorm,
+                                            moe_add_rmsnorm_bwd)
+
+
+class PreNormMoE:
+    """out = moe(norm(x + residual)); the sum x + residual goes on as the residual stream."""
+
+    def __init__(self, H: int, F: int, E: int, k: int, device="cuda", seed: int = 0):
+        g = torch.Generator(device=device).manual_seed(seed)
+
+        def normal(*shape, scale, dtype=torch.bfloat16):
+            return (torch.randn(*shape, generator=g, device=device) * scale).to(dtype)
+        self.H, self.F, self.E, self.k = H, F, E, k
+        self.norm_weight = torch.ones(H, dtype=torch.bfloat16, device=device)
+        self.W_router = normal(H, E, scale=H ** -0.5, dtype=torch.float32)
+        self.W = (normal(E, H, F, scale=0.02), normal(E, H, F, scale=0.02), normal(E, F, H, scale=0.02))
+        self.W_mx = MxWeights(*self.W)
+        self._decode: dict = {}
+
+    def router(self, y: torch.Tensor) -> torch.Tensor:
+        return y.float() @ self.W_router
+
+    def generate(self, x, residual, mx: bool = False):
+        """A few tokens (at most 64): (block output, new residual)."""
+        T = x.shape[0]
+        if (T, mx) not in self._decode:
+            layer = (MoeDecodeMX if mx else MoeDecode)(T, self.H, self.F, self.E, self.k, x.device)
+            self._decode[T, mx] = layer, NormOutput.empty(T, self.H, device=x.device)
+        layer, norm = self._decode[T, mx]
+        moe_add_rmsnorm(x, self.norm_weight, residual=residual, out=norm)
+        return layer(norm.y, self.router(norm.y), *((self.W_mx,) if mx else self.W)), norm.sum
+
+    def prompt(self, x, residual):
+        """Many tokens on MXFP8 rows and weights: (block output, new residual)."""
+        norm = moe_add_rmsnorm(x, self.norm_weight, residual=residual, bf16=True, mxfp8=True)
+        layer = MoeForwardMX(x.shape[0], self.H, self.F, self.E, self.k, x.device)
+        return layer((norm.y_q, norm.y_sf), self.router(norm.y), self.W_mx), norm.sum
+
+    def train_step(self, x, residual, d_out, d_residual):
+        """Forward and backward: (block output, gradient of x and of the residual, gradients by name)."""
+        norm = moe_add_rmsnorm(x, self.norm_weight, residual=residual)
+        logits = self.router(norm.y)
+        fwd = MoeForward(x.shape[0], self.H, self.F, self.E, self.k, x.device, keep_fc1_c=True)
+        out = fwd(norm.y, logits, *self.W)
+        bwd = MoeBackward(fwd, want_d_logits=True)
+        dy = bwd(d_out, *self.W, logits=logits)
+        # the router's projection reads the norm's output too
+        dy = (dy.float() + bwd.d_logits @ self.W_router.t()).to(torch.bfloat16)
+        dx, d_weight = moe_add_rmsnorm_bwd(dy, norm.sum, self.norm_weight, norm.rstd, d_sum=d_residual,
+                                           ws=NormWorkspace(x.shape[0], self.H, x.device))
+        grads = {"norm_weight": d_weight, "W_router": norm.y.float().t() @ bwd.d_logits, "W_gate": bwd.dW_gate,
+                 "W_up": bwd.dW_up, "W_down": bwd.dW_down}
+        return out, dx, grads
+
+
+def main():
+    block = PreNormMoE(H=1024, F=512, E=16, k=4)
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def rows(T):
+        return torch.randn(T, block.H, generator=g, device="cuda").to(torch.bfloat16)
+    x, r = rows(300), rows(300)
+    prompt, _ = block.prompt(x, r)
+    few, _ = block.generate(x[:5].contiguous(), r[:5].contiguous())
+    few_mx, stream = block.generate(x[:5].contiguous(), r[:5].contiguous(), mx=True)
+    out, dx, grads = block.train_step(x, r, rows(300), rows(300))
+
+    def off(a, b):
+        return float((a.float() - b.float()).norm() / b.float().norm())
+    print(f"generation against the training forward: bf16 {off(few, out[:5]):.1e}, MXFP8 weights {off(few_mx, out[:5]):.1e}")
+    print(f"prompt on MXFP8 rows and weights against it: {off(prompt, out):.1e}")
+    print("gradients:", ", ".join(f"{n} {float(v.float().norm()):.3g}" for n, v in grads.items()),
+          f"dx {float(dx.float().norm()):.3g}")
+
+
+if __name__ == "__main__":
+    main()
