@@ -364,32 +364,33 @@ class MoeDecode:
         self.router, self.expert_bias, self.normalize = router, expert_bias, normalize
         dev = torch.device(device)
         self.device = dev
+        self.score_fn = SCORE_SIGMOID if router == "sigmoid" else SCORE_SOFTMAX
         self.ws = DecodeWorkspace(T, H, F, E, k, dev)
         self._out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
         self._idx = torch.empty(T, k, dtype=torch.int32, device=dev)
         self._w = torch.empty(T, k, dtype=torch.float32, device=dev)
         self.out, self.topk_idx, self.topk_w = self._out, self._idx, self._w
 
-    def _args(self, x, stream):
+    def _run(self, call, x, logits, weights, stream):
         t = x.shape[0]
         if t > self.T:
             raise ValueError(f"at most {self.T} tokens a call, got {t}")
         if t != self.out.shape[0]:
             self.out, self.topk_idx, self.topk_w = self._out[:t], self._idx[:t], self._w[:t]
-        return dict(ws=self.ws, score_fn=SCORE_SIGMOID if self.router == "sigmoid" else SCORE_SOFTMAX,
-                    expert_bias=self.expert_bias, normalize=self.normalize, clamp=self.swiglu_clamp,
-                    topk_idx=self.topk_idx, topk_w=self.topk_w, out=self.out, stream=stream)
+        call(x, logits, *weights, self.k, self.ws, self.score_fn, self.expert_bias, self.normalize, self.swiglu_clamp,
+             self.topk_idx, self.topk_w, self.out, stream)
+        return self.out
 
     def __call__(self, x, logits, W_gate, W_up, W_down, stream=None):
-        return moe_decode(x, logits, W_gate, W_up, W_down, self.k, **self._args(x, stream))[0]
+        return self._run(moe_decode, x, logits, (W_gate, W_up, W_down), stream)
 
 
 class MoeDecodeMX(MoeDecode):
     """MoeDecode on MXFP8 expert weights (MxWeights); x and the hidden activations stay unquantised."""
 
     def __call__(self, x, logits, w: MxWeights, stream=None):
-        return moe_decode_mxfp8(x, logits, w.Wg_q, w.Wg_sf, w.Wu_q, w.Wu_sf, w.Wd_q, w.Wd_sf, self.F, self.k,
-                                **self._args(x, stream))[0]
+        return self._run(moe_decode_mxfp8, x, logits, (w.Wg_q, w.Wg_sf, w.Wu_q, w.Wu_sf, w.Wd_q, w.Wd_sf, self.F),
+                         stream)
 
 
 class HostPipeline:
