@@ -194,6 +194,12 @@ __device__ __forceinline__ void count_release(uint32_t *p, uint32_t n) {
 __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t &r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
 }
+// Eight consecutive columns.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
 // Waits for this thread's TMEM loads; the registers pass through, so that no use moves ahead.
 __device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -795,30 +801,29 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
                         swiglu(__uint_as_float(y[0]) + __uint_as_float(y[2]),
                                __uint_as_float(y[1]) + __uint_as_float(y[3]), a));
             }
-            for (int i0 = 0; !direct && i0 < s.cnt; i0 += 8) {
+            // eight columns at a time, those groups that hold a token of the expert
+            const int cols = s.down ? s.cnt : a.T;
+            for (int c0 = 0; !direct && c0 < cols; c0 += 8) {
+                const uint32_t bits = s.down ? 0xFFu >> (cols - c0 < 8 ? 8 - (cols - c0) : 0) : (uint32_t)(m >> c0) & 0xFFu;
+                if (!bits) continue;
                 uint32_t y0[8] = {}, y1[8] = {}, z0[8] = {}, z1[8] = {};
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (i0 + j < s.cnt) {
-                        const uint32_t c = s.down ? i0 + j : __ffsll((long long)m) - 1;
-                        m &= m - 1;
-                        tmem_ld1(d0 + c, y0[j]);
-                        if (two) tmem_ld1(d1 + c, y1[j]);
-                        if (terms) {
-                            tmem_ld1(d0 + second + c, z0[j]);
-                            if (two) tmem_ld1(d1 + second + c, z1[j]);
-                        }
-                    }
+                tmem_ld8(d0 + c0, y0);
+                if (two) tmem_ld8(d1 + c0, y1);
+                if (terms) {
+                    tmem_ld8(d0 + second + c0, z0);
+                    if (two) tmem_ld8(d1 + second + c0, z1);
+                }
                 tmem_ld_wait8(y0);
                 tmem_ld_wait8(y1);
                 tmem_ld_wait8(z0);
                 tmem_ld_wait8(z1);
+                float *p = part + (size_t)(s.down ? c0 : __popcll(m & ((1ull << c0) - 1))) * step;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (i0 + j < s.cnt) {
-                        float *p = part + (size_t)(i0 + j) * step;
+                    if (bits >> j & 1) {
                         p[0] = __uint_as_float(y0[j]) + __uint_as_float(z0[j]);
                         if (two) p[128] = __uint_as_float(y1[j]) + __uint_as_float(z1[j]);
+                        p += step;
                     }
             }
             sm100::tc_fence_before();
@@ -895,23 +900,34 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
         int g = 1;
         while (g < 32 && quads * g * 2 <= threads) g *= 2;
         const int sub = lane & (g - 1);
-        const int terms = a.k * S2;
+        const int most = pc.down > pc.last ? pc.down : pc.last, terms = a.k * most;
         for (int v0 = 0; v0 < quads; v0 += threads / g) {
             const int v = v0 + (cta * kDecThreads + (int)threadIdx.x) / g;
             float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             const int t = v / (a.H / 4), c4 = v - t * (a.H / 4), nt = c4 / 64;
-            if (v < quads) {
-#pragma unroll 4
-                for (int i = sub; i < terms; i += g) {
-                    const int j = i / S2, piece = i - j * S2, r = s_route[t * a.k + j];
-                    if (piece >= (r >= last_r0 ? pc.last : pc.down)) continue;
-                    const float w = s_w[t * a.k + j];
-                    const float4 p = __ldcg(reinterpret_cast<const float4 *>(
-                        a.part2 + (((size_t)r * NT + nt) * S2 + piece) * 256 + (c4 - nt * 64) * 4));
-                    s.x += w * p.x;
-                    s.y += w * p.y;
-                    s.z += w * p.z;
-                    s.w += w * p.w;
+            for (int i0 = sub; v < quads && i0 < terms; i0 += 4 * g) {   // four loads in flight
+                float w[4];
+                float4 p[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int i = i0 + u * g, j = i / most, piece = i - j * most;
+                    w[u] = 0.0f;
+                    p[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (i < terms) {
+                        const int r = s_route[t * a.k + j];
+                        if (piece < (r >= last_r0 ? pc.last : pc.down)) {
+                            w[u] = s_w[t * a.k + j];
+                            p[u] = __ldcg(reinterpret_cast<const float4 *>(
+                                a.part2 + (((size_t)r * NT + nt) * S2 + piece) * 256 + (c4 - nt * 64) * 4));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    s.x += w[u] * p[u].x;
+                    s.y += w[u] * p[u].y;
+                    s.z += w[u] * p[u].z;
+                    s.w += w[u] * p[u].w;
                 }
             }
             for (int off = g >> 1; off > 0; off >>= 1) {
