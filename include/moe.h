@@ -635,7 +635,7 @@ MOE_API moe_status_t moe_dequantize_weights_mxfp8(const uint8_t *data, const uin
  *   y_q,y_sf device uint8 [T, H] E4M3 codes and [T, H/32] UE8M0 scale bytes out
  *            (row-major; the MX rule of the MXFP8 section), or both NULL
  *   rstd     device fp32 [T] out, or NULL; needed by the backward
- * At least one of y and y_q / y_sf.  A row of zeros gives y = 0.
+ * At least one of y and y_q / y_sf.  With eps > 0 a row of zeros gives y = 0.
  *
  * Limits: H % 8 == 0 (H % 32 == 0 with y_q), H <= 32768, T < 2^31; the bf16 tensors
  * 16-byte and y_q 8-byte aligned.  T = 0 is a no-op.  Errors: MOE_ERR_INVALID_ARG
@@ -672,8 +672,8 @@ MOE_API moe_status_t moe_add_rmsnorm_bwd(const moe_bf16_t *dy, const moe_bf16_t 
 
 /* moe_permute_mxfp8 for rows that are already MXFP8 (moe_add_rmsnorm's y_q / y_sf):
  *   rows_q  device uint8 [T, H] E4M3 codes; rows_sf device uint8 [T, H/32] scale bytes
- * The codes are copied and the scale bytes take the tile layout (zeros in the rows of a
- * tile past its group's end); every other argument, output and limit as moe_permute_mxfp8
+ * The codes are copied and the scale bytes take the tile layout (the rows of a tile past its
+ * group's end get zeros or keep what they held); every other argument, output and limit as moe_permute_mxfp8
  * (rows_q, x_q and x_sf 16-byte, rows_sf 4-byte aligned). */
 MOE_API moe_status_t moe_permute_rows_mxfp8(const uint8_t *rows_q, const uint8_t *rows_sf, const int32_t *topk_idx,
                                             int64_t T, int H, int E, int k, uint8_t *x_q, uint8_t *x_sf,

@@ -798,6 +798,11 @@ def moe_permute_rows_mxfp8(rows_q: torch.Tensor, rows_sf: torch.Tensor, topk_idx
     dev = rows_q.get_device()
     if out is None:
         out = PermutationMX.empty(T, H, E, k, rows_q.device)
+    elif (out.rows_cap < T * k or out.x_q.shape != (out.rows_cap, H) or out.dst_of_route.shape != (T, k)
+          or out.src_of_row.shape != (out.rows_cap,) or out.group_sizes.shape != (E,)
+          or out.group_offsets.shape != (E + 1,)
+          or out.x_sf.numel() < ((out.rows_cap + 127) // 128 + E) * (H // 128) * 512):
+        raise ValueError(f"out: not the buffers of PermutationMX.empty({T}, {H}, {E}, {k})")
     st = load_library().moe_permute_rows_mxfp8(
         _addr(rows_q, "rows_q", torch.uint8, (T, H), dev), _addr(rows_sf, "rows_sf", torch.uint8, (T, H // 32), dev),
         _addr(topk_idx, "topk_idx", torch.int32, (T, k), dev), T, H, E, k, out.x_q.data_ptr(), out.x_sf.data_ptr(),

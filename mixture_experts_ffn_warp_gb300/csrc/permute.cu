@@ -342,7 +342,7 @@ permute_scan_kernel(int32_t *__restrict__ chunk_counts, int64_t chunks, int E, i
     scan_groups(chunk_counts, chunks, E, align, group_sizes, group_offsets, mtile_start, nullptr);
 }
 
-// ---- counting pass in one thread-block cluster (R <= kClusterRoutes) ----
+// ---- counting pass in one thread-block cluster ----
 // The CTAs of one cluster exchange their per-expert counts through distributed shared
 // memory instead of global memory, a fence and a finished-blocks counter, and every CTA
 // writes the final rows of its own routes: the scatter then only reads them.  Measured on
@@ -352,7 +352,9 @@ permute_scan_kernel(int32_t *__restrict__ chunk_counts, int64_t chunks, int E, i
 // the limit of 16 warps.
 constexpr int kClusterCtas = 8;                                          // portable cluster size
 constexpr int kClusterMaxWarps = 16;
-constexpr int64_t kClusterRoutes = (int64_t)kClusterCtas * kClusterMaxWarps * 32 * kPermSteps;   // 32768
+constexpr int kWideCtas = 16;                                            // non-portable, opt-in
+constexpr int64_t kCtaRoutes = (int64_t)kClusterMaxWarps * 32 * kPermSteps;   // 4096
+constexpr int64_t kClusterRoutes = kWideCtas * kCtaRoutes;               // 65536
 
 __device__ __forceinline__ uint32_t cta_rank_in_cluster() {
     uint32_t r;
@@ -418,13 +420,15 @@ permute_count_cluster_kernel(const int32_t *__restrict__ topk_idx, int64_t R, in
     for (int i = 0; i < 4; ++i) {
         const int e = e0 + i;
         if (i < per && e < E) {
-            int v[kClusterCtas];
+            for (int c0 = 0; c0 < (int)C; c0 += kClusterCtas) {   // eight loads in flight
+                int v[kClusterCtas];
 #pragma unroll
-            for (int c = 0; c < kClusterCtas; ++c) v[c] = c < (int)C ? ld_cluster_s32(s_tot + e, c) : 0;
+                for (int c = 0; c < kClusterCtas; ++c) v[c] = c0 + c < (int)C ? ld_cluster_s32(s_tot + e, c0 + c) : 0;
 #pragma unroll
-            for (int c = 0; c < kClusterCtas; ++c) {
-                if (c < (int)me) pre[i] += v[c];
-                tot[i] += v[c];
+                for (int c = 0; c < kClusterCtas; ++c) {
+                    if (c0 + c < (int)me) pre[i] += v[c];
+                    tot[i] += v[c];
+                }
             }
         }
     }
@@ -501,15 +505,22 @@ permute_count_cluster_kernel(const int32_t *__restrict__ topk_idx, int64_t R, in
     cluster_wait();   // no CTA leaves while another may still read its totals
 }
 
-// Warps per CTA of the cluster counting pass for R routes, 0 when R does not fit it
-// (dyn_smem_max: the dynamic shared memory a CTA may take).
-int cluster_count_warps(int64_t R, int E, size_t dyn_smem_max) {
-    if (R <= 0) return 0;
-    const int64_t ctas = (R + kPermChunk - 1) / kPermChunk < kClusterCtas ? (R + kPermChunk - 1) / kPermChunk
-                                                                            : kClusterCtas;
+// CTAs of the cluster counting pass for R routes (one per 2048 up to 8; above 32768 routes, 16
+// CTAs of up to 4096 each), and its warps per CTA, 0 when R does not fit it (dyn_smem_max: the
+// dynamic shared memory a CTA may take).  The 16-CTA cluster is for moe_permute_rows_mxfp8 alone
+// (`wide`): it saves that call 2.7 us at 65536 routes and 16 at 33600 routes to 1024 experts, while
+// moe_permute_mxfp8, whose scatter then looks its tiles up itself, lost 4 us on the DeepSeek-V3 shape.
+int cluster_ctas(int64_t R) {
+    if (R > kClusterCtas * kCtaRoutes) return (int)((R + kCtaRoutes - 1) / kCtaRoutes);
+    const int64_t c = (R + kPermChunk - 1) / kPermChunk;
+    return (int)(c < kClusterCtas ? c : kClusterCtas);
+}
+int cluster_count_warps(int64_t R, int E, size_t dyn_smem_max, bool wide) {
+    if (R <= 0 || R > (wide ? kClusterRoutes : kClusterCtas * kCtaRoutes)) return 0;
+    const int64_t ctas = cluster_ctas(R);
     int64_t w = (R + ctas * 32 * kPermSteps - 1) / (ctas * 32 * kPermSteps);
     if (w < kPermWarps) w = kPermWarps;
-    if (w > kClusterMaxWarps || R > kClusterRoutes) return 0;
+    if (w > kClusterMaxWarps) return 0;
     if ((size_t)(w * E + 2 * E) * sizeof(int32_t) > dyn_smem_max) return 0;
     return (int)w;
 }
@@ -521,7 +532,7 @@ int cluster_count_warps(int64_t R, int E, size_t dyn_smem_max) {
 moe_status_t count_and_scan(const int32_t *topk_idx, int64_t R, int E, int align, int64_t rows_cap,
                             int32_t *dst_of_route, int32_t *src_of_row, int32_t *counts, int32_t *group_sizes,
                             int32_t *group_offsets, int32_t *mtile, uint32_t *done, uint32_t *err, cudaStream_t s,
-                            bool *final_rows) {
+                            bool *final_rows, bool wide = false) {
     int32_t *local_rank = dst_of_route;
     const int64_t chunks = perm_chunks(R);
     *final_rows = false;
@@ -535,14 +546,20 @@ moe_status_t count_and_scan(const int32_t *topk_idx, int64_t R, int E, int align
         cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
         return MOE_ERR_CUDA;
     const size_t dyn = optin > 1024 ? (size_t)optin - 1024 : 0;   // (static arrays: 256 bytes)
-    const int w = cluster_count_warps(R, E, dyn);
+    const int w = cluster_count_warps(R, E, dyn, wide);
     if (w > 0) {
         if (cudaFuncSetAttribute(permute_count_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)dyn) != cudaSuccess) {
             (void)cudaGetLastError();   // refused: not this call's error, the chunked pass runs
             goto chunked;
         }
-        const int ctas = (int)(chunks < kClusterCtas ? chunks : kClusterCtas);
+        const int ctas = cluster_ctas(R);
+        if (ctas > kClusterCtas &&
+            cudaFuncSetAttribute(permute_count_cluster_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                cudaSuccess) {
+            (void)cudaGetLastError();
+            goto chunked;
+        }
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)ctas);
         cfg.blockDim = dim3((unsigned)(w * 32));
@@ -1038,11 +1055,11 @@ extern "C" moe_status_t moe_permute_mxfp8(const moe_bf16_t *x, const int32_t *to
 // token, as many written per route.
 //
 // The codes go by token (a warp holds the row in registers and stores it k times), the scales
-// by destination tile: a row's scale words lie 512 bytes apart in the tile layout, and
-// stored from the token's warp, 4 bytes each, they cost as much as a quarter of all the codes.
-// Gathered by tile through shared memory they leave as whole 512-byte atoms, beside the codes.
-// 8192 x 7168 to 8 of 256 experts: the scatter alone 83 us for the codes, 106 with the
-// scales from the token's warp.
+// by destination tile where tiles are not too sparse: a row's scale words lie 512 bytes apart
+// in the tile layout, and stored from the token's warp, 4 bytes each, they cost as much as a
+// quarter of all the codes.  Gathered by tile through shared memory they leave as whole 512-byte
+// atoms, beside the codes.  8192 x 7168 to 8 of 256 experts: 99 us (547 MB, 81 us at the copy
+// rate; the codes alone 83 us, the counting pass before them 11), 109 with the scales by token.
 // ---------------------------------------------------------------------------
 
 namespace moe {
@@ -1071,35 +1088,37 @@ permute_place_kernel(const int32_t *__restrict__ topk_idx, int64_t R, int E, con
 
 constexpr int kSlab = 64;   // 128-element K blocks of a tile's scales in shared memory at a time
 
-// The scales of one 128-row tile, gathered by the whole block: s_tok[m] is the token of row m
-// (-1: none, zeros); s_sf holds SLAB 128-element K blocks of it at a time.
+// The scales of one 128-row tile, gathered by the whole block: s_tok[m] is the token of row
+// m < rows (the rest of the tile gets zeros); s_sf holds SLAB 128-element K blocks of it at a time.
 template <int SLAB>
-__device__ __forceinline__ void gather_tile_scales(const uint32_t *__restrict__ rows_sf, const int *s_tok, int tile,
-                                                   int kb128, uint32_t *s_sf, uint32_t *__restrict__ x_sf) {
+__device__ __forceinline__ void gather_tile_scales(const uint32_t *__restrict__ rows_sf, const int *s_tok, int rows,
+                                                   int tile, int kb128, uint32_t *s_sf, uint32_t *__restrict__ x_sf) {
     const int lane = threadIdx.x & 31;
     for (int b0 = 0; b0 < kb128; b0 += SLAB) {
         const int nb = kb128 - b0 < SLAB ? kb128 - b0 : SLAB;
-        for (int m = threadIdx.x >> 5; m < 128; m += kScatterWarps) {
-            const int t = s_tok[m];
-            for (int b = lane; b < nb; b += 32) {
-                uint32_t *to = s_sf + m * (SLAB + 1) + b;
-                if (t >= 0)   // all of the slab's words in flight at once
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
-                                     static_cast<uint32_t>(__cvta_generic_to_shared(to))),
-                                 "l"(rows_sf + (int64_t)t * kb128 + b0 + b)
+#pragma unroll 4
+        for (int m0 = 0; m0 < 128; m0 += kScatterWarps) {
+            const int m = m0 + (threadIdx.x >> 5);
+            if (m >= rows) break;
+            const uint32_t *from = rows_sf + (int64_t)s_tok[m] * kb128 + b0;
+#pragma unroll
+            for (int b1 = 0; b1 < SLAB; b1 += 32)   // all of the slab's words in flight at once
+                if (b1 + lane < nb)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(static_cast<uint32_t>(
+                                     __cvta_generic_to_shared(s_sf + m * (SLAB + 1) + b1 + lane))),
+                                 "l"(from + b1 + lane)
                                  : "memory");
-                else
-                    *to = 0u;
-            }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
         // 16 bytes of an atom: rows i, i + 32, i + 64, i + 96
         for (int v = threadIdx.x; v < nb * 32; v += blockDim.x) {
             const int b = v >> 5, i = v & 31;
-            const uint32_t *p = s_sf + i * (SLAB + 1) + b;
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] = i + 32 * q < rows ? s_sf[(i + 32 * q) * (SLAB + 1) + b] : 0u;
             *reinterpret_cast<uint4 *>(x_sf + ((int64_t)tile * kb128 + b0 + b) * 128 + i * 4) =
-                make_uint4(p[0], p[32 * (SLAB + 1)], p[64 * (SLAB + 1)], p[96 * (SLAB + 1)]);
+                make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncthreads();
     }
@@ -1133,10 +1152,11 @@ __device__ __forceinline__ void copy_row(const uint4 *__restrict__ row, int vecs
 }
 
 // Blocks below scale_blocks: the scales of one 128-row tile each.  The others: the codes of
-// kScatterWarps tokens.
+// kScatterWarps tokens, and their scales too where scale_blocks is 0.
 __global__ void __launch_bounds__(kScatterWarps * 32)
-permute_rows_mx_kernel(const uint4 *__restrict__ rows_q, const uint32_t *__restrict__ rows_sf, int64_t T, int k, int E,
-                       int H, const int32_t *__restrict__ group_offsets, const int32_t *__restrict__ mtile_start,
+permute_rows_mx_kernel(const uint4 *__restrict__ rows_q, const uint32_t *__restrict__ rows_sf,
+                       const int32_t *__restrict__ topk_idx, int64_t T, int k, int E, int H,
+                       const int32_t *__restrict__ group_offsets, const int32_t *__restrict__ mtile_start,
                        const int32_t *__restrict__ dst_of_route, const int32_t *__restrict__ src_of_row,
                        uint4 *__restrict__ x_q, uint32_t *__restrict__ x_sf, int64_t scale_blocks) {
     constexpr int SLAB = 64;
@@ -1152,12 +1172,11 @@ permute_rows_mx_kernel(const uint4 *__restrict__ rows_q, const uint32_t *__restr
         __syncthreads();
         const int e = s_group;
         if (e < 0) return;   // past the last tile
-        if (threadIdx.x < 128) {
-            const int row = group_offsets[e] + (tile - mtile_start[e]) * 128 + threadIdx.x;
-            s_tok[threadIdx.x] = row < group_offsets[e + 1] ? src_of_row[row] / k : -1;
-        }
+        const int row0 = group_offsets[e] + (tile - mtile_start[e]) * 128;
+        const int rows = min(group_offsets[e + 1] - row0, 128);
+        if ((int)threadIdx.x < rows) s_tok[threadIdx.x] = src_of_row[row0 + threadIdx.x] / k;
         __syncthreads();
-        gather_tile_scales<SLAB>(rows_sf, s_tok, tile, H / 128, s_sf, x_sf);
+        gather_tile_scales<SLAB>(rows_sf, s_tok, rows, tile, H / 128, s_sf, x_sf);
         return;
     }
     const int lane = threadIdx.x & 31, vecs = H / 16;
@@ -1166,7 +1185,25 @@ permute_rows_mx_kernel(const uint4 *__restrict__ rows_q, const uint32_t *__restr
     if (t < T) load_row_vecs(rows_q + t * vecs, 0, vecs, r);   // complete before the counting pass ran: no need to wait
     pdl_wait();
     if (t >= T) return;
-    copy_row(rows_q + t * vecs, vecs, k, lane < k ? dst_of_route[t * k + lane] : -1, r, x_q);
+    const int my_dst = lane < k ? dst_of_route[t * k + lane] : -1;
+    copy_row(rows_q + t * vecs, vecs, k, my_dst, r, x_q);
+    if (scale_blocks) return;
+    const int kb128 = H / 128;
+    int my_tile = 0, my_m = 0;
+    if (my_dst >= 0) {
+        const int e = topk_idx[t * k + lane], i = my_dst - group_offsets[e];
+        my_tile = mtile_start[e] + i / 128;
+        my_m = i % 128;
+    }
+    for (int b0 = 0; b0 < kb128; b0 += 32) {
+        const uint32_t word = b0 + lane < kb128 ? __ldg(rows_sf + t * kb128 + b0 + lane) : 0u;
+        for (int j = 0; j < k; ++j) {
+            const int dst = __shfl_sync(0xFFFFFFFFu, my_dst, j), tile = __shfl_sync(0xFFFFFFFFu, my_tile, j),
+                      m = __shfl_sync(0xFFFFFFFFu, my_m, j);
+            if (dst >= 0 && b0 + lane < kb128)
+                x_sf[mx::tile_sf_offset(tile, kb128, m, 4 * (b0 + lane)) / 4] = word;
+        }
+    }
 }
 
 // Up to kSmallRoutes routes: one kernel.  Every block ranks all the routes for itself in shared
@@ -1282,12 +1319,10 @@ permute_rows_small_kernel(const uint4 *__restrict__ rows_q, const uint32_t *__re
         __syncthreads();
         const int e = s_group;
         if (e < 0) return;   // past the last tile
-        if (tid < 128) {
-            const int row = s_off[e] + (tile - s_mt[e]) * 128 + tid;
-            s_tok[tid] = row < s_off[e + 1] ? s_src[row] / k : -1;
-        }
+        const int row0 = s_off[e] + (tile - s_mt[e]) * 128, rows = min(s_off[e + 1] - row0, 128);
+        if (tid < rows) s_tok[tid] = s_src[row0 + tid] / k;
         __syncthreads();
-        gather_tile_scales<SLAB>(rows_sf, s_tok, tile, H / 128, s_sf, x_sf);
+        gather_tile_scales<SLAB>(rows_sf, s_tok, rows, tile, H / 128, s_sf, x_sf);
         return;
     }
     const int t = ((int)blockIdx.x - scale_blocks) * kScatterWarps + warp, vecs = H / 16;
@@ -1326,9 +1361,9 @@ extern "C" moe_status_t moe_permute_rows_mxfp8(const uint8_t *rows_q, const uint
     int32_t *counts = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + kWsHeaderBytes);
     int32_t *mtile = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + kWsHeaderBytes + ws_counts_bytes(chunks, E));
     const int64_t scale_blocks = R / 128 + (R < E ? R : E);   // at least the tiles of any routing
-    const unsigned blocks = (unsigned)(scale_blocks + (T + kScatterWarps - 1) / kScatterWarps);
     if (R > 0 && R <= kSmallRoutes) {
-        launch_k(permute_rows_small_kernel, dim3(blocks), dim3(kScatterWarps * 32), small_smem(R, E), s,
+        launch_k(permute_rows_small_kernel, dim3((unsigned)(scale_blocks + (T + kScatterWarps - 1) / kScatterWarps)),
+                 dim3(kScatterWarps * 32), small_smem(R, E), s,
                  reinterpret_cast<const uint4 *>(rows_q), reinterpret_cast<const uint32_t *>(rows_sf), topk_idx, (int)T,
                  k, E, H, dst_of_route, src_of_row, group_sizes, group_offsets, reinterpret_cast<uint4 *>(x_q),
                  reinterpret_cast<uint32_t *>(x_sf), (int)scale_blocks, err);
@@ -1336,14 +1371,19 @@ extern "C" moe_status_t moe_permute_rows_mxfp8(const uint8_t *rows_q, const uint
     }
     bool final_rows = false;
     if (count_and_scan(topk_idx, R, E, 1, rows_cap, dst_of_route, src_of_row, counts, group_sizes, group_offsets, mtile,
-                       ws_done_counter(ws), err, s, &final_rows) != MOE_OK)
+                       ws_done_counter(ws), err, s, &final_rows, true) != MOE_OK)
         return MOE_ERR_CUDA;
     if (T == 0) return MOE_OK;
+    // Scales by tile where a tile holds 32 rows or more on average, else by token.  Measured: 114 rows
+    // (16384 x 4096, 8 of 128) 112 us by tile, 119 by token; 43 (8192 x 7168, 8 of 1024) 110 and 143;
+    // 26 (4200 x 512, 8 of 1024) 23.4 and 19.5; 8 (1024 x 7168, 8 of 1024) 34 and 22.
+    const int64_t by_tile = R >= 32 * scale_blocks ? scale_blocks : 0;
     if (!final_rows)
         launch_k(permute_place_kernel, dim3((unsigned)((R + 255) / 256)), dim3(256), 0, s, topk_idx, R, E, counts,
                  dst_of_route, src_of_row, rows_cap, err);
-    launch_k(permute_rows_mx_kernel, dim3(blocks), dim3(kScatterWarps * 32), 0, s, reinterpret_cast<const uint4 *>(rows_q),
-             reinterpret_cast<const uint32_t *>(rows_sf), T, k, E, H, group_offsets, mtile, dst_of_route, src_of_row,
-             reinterpret_cast<uint4 *>(x_q), reinterpret_cast<uint32_t *>(x_sf), scale_blocks);
+    launch_k(permute_rows_mx_kernel, dim3((unsigned)(by_tile + (T + kScatterWarps - 1) / kScatterWarps)),
+             dim3(kScatterWarps * 32), 0, s, reinterpret_cast<const uint4 *>(rows_q),
+             reinterpret_cast<const uint32_t *>(rows_sf), topk_idx, T, k, E, H, group_offsets, mtile, dst_of_route, src_of_row,
+             reinterpret_cast<uint4 *>(x_q), reinterpret_cast<uint32_t *>(x_sf), by_tile);
     return launch_status();
 }

@@ -249,7 +249,8 @@ def test_offsets_past_32_bits():
 
 @pytest.mark.parametrize("T,H,E,k", [(1, 128, 4, 1), (1, 7168, 256, 8), (100, 2048, 64, 6), (257, 384, 8, 2),
                                      (3000, 256, 5, 3), (70, 128, 40, 32), (5000, 512, 128, 8),
-                                     (64, 3200, 1024, 32), (1000, 9216, 3, 2), (16, 128, 1, 1)])
+                                     (64, 3200, 1024, 32), (1000, 9216, 3, 2), (16, 128, 1, 1),
+                                     (8192, 128, 256, 8), (2100, 640, 1024, 8), (4200, 256, 1024, 8)])
 def test_permute_rows_equals_quantising_permute(T, H, E, k):
     """Rows quantised first and permuted after = quantised by the permutation, bit for bit."""
     rows, _, _ = inputs(T, H, seed=T + E, residual=False)
@@ -287,6 +288,8 @@ def test_permute_rows_bad_id_and_empty():
     assert (p.group_sizes == 0).all()
     with pytest.raises(ValueError):
         moe_permute_rows_mxfp8(q, sf[:, :2].contiguous(), idx, E, ws)
+    with pytest.raises(ValueError):
+        moe_permute_rows_mxfp8(q, sf, idx, E, ws, out=PermutationMX.empty(T - 1, H, E, k))   # too small
 
 
 def test_forward_mx_takes_quantised_rows():
