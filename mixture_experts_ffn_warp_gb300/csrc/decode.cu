@@ -38,10 +38,10 @@
 // partial sums, output): 12.5 us for the smallest.
 //
 // A CTA's roles: a warp that draws segments and loads their weights as long as the ring has
-// room, a warp that loads the small operand (x, then h) and is the only one that waits for
-// another CTA, a warp that issues the MMAs, four that drain the accumulators, four that join.
+// room, a warp that loads the small operand (x, then an expert's h once it is complete), a warp
+// that issues the MMAs, four that drain the accumulators, four that join.
 //
-// Precision.  On bf16 weights h enters phase 2 as two bf16 terms hi + lo in separate columns
+// Precision.  On bf16 weights h enters the down product as two bf16 terms hi + lo in separate columns
 // (N is padded to 16 anyway), so no rounding below fp32 precedes the output's.  On MXFP8
 // weights x and h enter as two E4M3 terms each, the second of the first's remainder with its
 // own block scales: x is then exact but for elements 2^-15 below their block's largest, h has
