@@ -717,19 +717,24 @@ class NormOutput:
                    rstd=buf(True, T, dtype=torch.float32))
 
 
-def _need2d(t, name: str, dtype: torch.dtype):
-    if not (isinstance(t, torch.Tensor) and t.dim() == 2 and t.get_device() >= 0):
-        _need(t, name, dtype)
-        raise ValueError(f"{name} must have two dimensions")
+def _rows(t, name: str, dtype: torch.dtype):
+    """(shape, device index, address) of a contiguous CUDA tensor [rows, columns] of this dtype."""
+    try:
+        shape, dev = t.shape, t.get_device()
+        if t.dtype is dtype and len(shape) == 2 and dev >= 0 and t.is_contiguous():
+            return shape, dev, t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, dtype)
+    raise ValueError(f"{name} must have two dimensions")
 
 
 def moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
                     out: NormOutput | None = None, bf16: bool = True, mxfp8: bool = False, stream=None) -> NormOutput:
     """sum = x + residual, y = sum * rstd * weight in bf16 and / or MXFP8 along H (moe.h).
     out: buffers of an earlier NormOutput.empty (which also says which outputs are wanted)."""
-    _need2d(x, "x", torch.bfloat16)
-    T, H = rows = x.shape
-    dev = x.get_device()
+    rows, dev, px = _rows(x, "x", torch.bfloat16)
+    T, H = rows
     if out is None:
         out = NormOutput.empty(T, H, bf16, mxfp8, residual is not None, x.device)
     r = s = y = q = sf = None
@@ -742,7 +747,7 @@ def moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, re
         q = _addr(out.y_q, "out.y_q", torch.uint8, rows, dev)
         sf = _addr(out.y_sf, "out.y_sf", torch.uint8, (T, H // 32), dev)
     st = load_library().moe_add_rmsnorm(
-        _addr(x, "x", torch.bfloat16, rows, dev), r, _addr(weight, "weight", torch.bfloat16, (H,), dev), eps, T, H, s, y,
+        px, r, _addr(weight, "weight", torch.bfloat16, (H,), dev), eps, T, H, s, y,
         q, sf, _addr(out.rstd, "out.rstd", torch.float32, (T,), dev), _stream_on(stream, dev))
     if st:
         raise MoeError("moe_add_rmsnorm", st)
@@ -766,9 +771,8 @@ def moe_add_rmsnorm_bwd(dy: torch.Tensor, sum: torch.Tensor, weight: torch.Tenso
                         want_dweight: bool = True, stream=None):
     """Gradient of moe_add_rmsnorm (moe.h): (dx bf16 [T, H] of x and the residual alike,
     dweight fp32 [H] or None).  sum: the forward's sum (its x where it had no residual)."""
-    _need2d(dy, "dy", torch.bfloat16)
-    T, H = rows = dy.shape
-    dev = dy.get_device()
+    rows, dev, pdy = _rows(dy, "dy", torch.bfloat16)
+    T, H = rows
     if dx is None:
         dx = torch.empty(T, H, dtype=torch.bfloat16, device=dy.device)
     if dweight is None and want_dweight:
@@ -776,7 +780,7 @@ def moe_add_rmsnorm_bwd(dy: torch.Tensor, sum: torch.Tensor, weight: torch.Tenso
     if dweight is not None and ws is None:
         ws = NormWorkspace(T, H, dy.device)
     st = load_library().moe_add_rmsnorm_bwd(
-        _addr(dy, "dy", torch.bfloat16, rows, dev),
+        pdy,
         None if d_sum is None else _addr(d_sum, "d_sum", torch.bfloat16, rows, dev),
         _addr(sum, "sum", torch.bfloat16, rows, dev), _addr(weight, "weight", torch.bfloat16, (H,), dev),
         _addr(rstd, "rstd", torch.float32, (T,), dev), T, H, _addr(dx, "dx", torch.bfloat16, rows, dev),
@@ -791,11 +795,10 @@ def moe_permute_rows_mxfp8(rows_q: torch.Tensor, rows_sf: torch.Tensor, topk_idx
                            out: PermutationMX | None = None, stream=None) -> PermutationMX:
     """moe_permute_mxfp8 for rows that are already MXFP8: codes uint8 [T, H], row-major
     scales uint8 [T, H/32] (moe.h)."""
-    _need2d(rows_q, "rows_q", torch.uint8)
-    _need2d(topk_idx, "topk_idx", torch.int32)
-    T, H = rows_q.shape
-    k = topk_idx.shape[1]
-    dev = rows_q.get_device()
+    (T, H), dev, pq = _rows(rows_q, "rows_q", torch.uint8)
+    (Ti, k), devi, pidx = _rows(topk_idx, "topk_idx", torch.int32)
+    if Ti != T or devi != dev:
+        raise ValueError(f"topk_idx must be [{T}, k] on {rows_q.device}")
     if out is None:
         out = PermutationMX.empty(T, H, E, k, rows_q.device)
     elif (out.rows_cap < T * k or out.x_q.shape != (out.rows_cap, H) or out.dst_of_route.shape != (T, k)
@@ -804,8 +807,7 @@ def moe_permute_rows_mxfp8(rows_q: torch.Tensor, rows_sf: torch.Tensor, topk_idx
           or out.x_sf.numel() < ((out.rows_cap + 127) // 128 + E) * (H // 128) * 512):
         raise ValueError(f"out: not the buffers of PermutationMX.empty({T}, {H}, {E}, {k})")
     st = load_library().moe_permute_rows_mxfp8(
-        _addr(rows_q, "rows_q", torch.uint8, (T, H), dev), _addr(rows_sf, "rows_sf", torch.uint8, (T, H // 32), dev),
-        _addr(topk_idx, "topk_idx", torch.int32, (T, k), dev), T, H, E, k, out.x_q.data_ptr(), out.x_sf.data_ptr(),
+        pq, _addr(rows_sf, "rows_sf", torch.uint8, (T, H // 32), dev), pidx, T, H, E, k, out.x_q.data_ptr(), out.x_sf.data_ptr(),
         out.rows_cap, out.dst_of_route.data_ptr(), out.src_of_row.data_ptr(), out.group_sizes.data_ptr(),
         out.group_offsets.data_ptr(), ws.buf.data_ptr(), ws.nbytes, _stream_on(stream, dev))
     if st:
@@ -839,9 +841,8 @@ _NO_CLAMP = (float("-inf"), float("inf"), float("-inf"), float("inf"))
 
 def _decode(fn, x, logits, weights, F, E, k, ws, score_fn, expert_bias, normalize, clamp, topk_idx, topk_w, out, stream):
     """Checks and call shared by moe_decode and moe_decode_mxfp8; weights(H, dev): their addresses."""
-    _need2d(x, "x", torch.bfloat16)
-    T, H = x.shape
-    dev = x.get_device()
+    rows, dev, px = _rows(x, "x", torch.bfloat16)
+    T, H = rows
     if topk_idx is None:
         topk_idx = torch.empty(T, k, dtype=torch.int32, device=x.device)
     if topk_w is None:
@@ -849,11 +850,11 @@ def _decode(fn, x, logits, weights, F, E, k, ws, score_fn, expert_bias, normaliz
     if out is None:
         out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
     st = getattr(load_library(), fn)(
-        _addr(x, "x", torch.bfloat16, (T, H), dev), _addr(logits, "logits", torch.float32, (T, E), dev),
+        px, _addr(logits, "logits", torch.float32, (T, E), dev),
         None if expert_bias is None else _addr(expert_bias, "expert_bias", torch.float32, (E,), dev), score_fn,
         1 if normalize else 0, *(_NO_CLAMP if clamp is None else clamp), *weights(H, dev), T, H, F, E, k,
         _addr(topk_idx, "topk_idx", torch.int32, (T, k), dev), _addr(topk_w, "topk_w", torch.float32, (T, k), dev),
-        _addr(out, "out", torch.bfloat16, (T, H), dev), ws.buf.data_ptr(), ws.nbytes, _stream_on(stream, dev))
+        _addr(out, "out", torch.bfloat16, rows, dev), ws.buf.data_ptr(), ws.nbytes, _stream_on(stream, dev))
     if st:
         raise MoeError(fn, st)
     return out, topk_idx, topk_w
