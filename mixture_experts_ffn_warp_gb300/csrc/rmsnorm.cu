@@ -30,6 +30,11 @@ namespace {
 constexpr int kNormMaxH = 32768;
 constexpr int kNormSms = 152;        // blocks are counted in multiples of this (dw's sum follows them)
 constexpr int kNormMaxThreads = 512;
+// Up to this many rows (and H / 4: a column block has H / 64 groups of threads for them) dw is
+// summed in the one launch.  Measured, GPU time of one launch and of two: 333 x 2048 4.2 us and 5.6,
+// 333 x 7168 6.7 and 8.2, 33 x 520 1.8 and 3.0; beyond, 600 x 7168 13.1 and 11.1, 333 x 520 7.1 and 4.6.
+// The host's time falls from 8.1 to 6.3 us a call.
+constexpr int kDirectRows = 400;
 
 // Packed pairs of fp32 (one instruction for two operations).
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -187,14 +192,47 @@ add_rmsnorm_kernel(const uint4 *x, const uint4 *res, const uint4 *__restrict__ w
     }
 }
 
-// dx of the rows blockIdx.x, blockIdx.x + gridDim.x, ..., and this block's share of dw, summed
-// in registers over its rows.  Up to V = 2 a thread keeps the products w dy and the row's s
+// dw of 64 columns, from all rows (small problems: dw needs no row sum, so these blocks run beside
+// those of dx and read dy and s a second time, from the L2): groups of 8 threads (8 columns
+// each) take every (threads / 8)-th row, then the groups are added in order.
+__device__ __forceinline__ void dw_columns(const uint4 *__restrict__ dy, const uint4 *__restrict__ sum,
+                                           const float *__restrict__ rstd_in, int T, int nv, int block,
+                                           float (*s_part)[64], float *__restrict__ dw) {
+    const int c = block * 8 + (threadIdx.x & 7), grp = threadIdx.x >> 3, groups = blockDim.x >> 3;
+    float2 acc[4] = {};
+    if (c < nv) {
+#pragma unroll 4
+        for (int row = grp; row < T; row += groups) {
+            float2 g[4], x[4];
+            unpack4(__ldg(dy + (int64_t)row * nv + c), g);
+            unpack4(__ldg(sum + (int64_t)row * nv + c), x);
+            const float r = __ldg(rstd_in + row);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] = fma2(g[j], mul2(x[j], make_float2(r, r)), acc[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        s_part[grp][(threadIdx.x & 7) * 8 + 2 * j] = acc[j].x;
+        s_part[grp][(threadIdx.x & 7) * 8 + 2 * j + 1] = acc[j].y;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 64; i += blockDim.x)
+        if (block * 64 + i < nv * 8) {
+            float t = 0.0f;
+            for (int k = 0; k < groups; ++k) t += s_part[k][i];
+            dw[block * 64 + i] = t;
+        }
+}
+
+// dx of the rows blockIdx.x, blockIdx.x + row_blocks, ..., and this block's share of dw, summed
+// in registers over its rows.  Blocks from row_blocks on: dw_columns.  Up to V = 2 a thread keeps the products w dy and the row's s
 // between the dot product and dx; above, it reads them again from shared memory.
 template <int V, int S>
 __global__ void __launch_bounds__(kNormMaxThreads)
 add_rmsnorm_bwd_kernel(const uint4 *dy, const uint4 *d_sum, const uint4 *__restrict__ sum,
                        const uint4 *__restrict__ weight, const float *__restrict__ rstd_in, int64_t T, int H,
-                       uint4 *dx, float *__restrict__ dw_part) {
+                       uint4 *dx, float *__restrict__ dw_part, int row_blocks, float *__restrict__ dw_direct) {
     constexpr bool KEEP = V <= 2;
     constexpr int KV = KEEP ? V : 1;
     extern __shared__ uint4 s_rows[];   // [S][3][V][threads]
@@ -203,6 +241,11 @@ add_rmsnorm_bwd_kernel(const uint4 *dy, const uint4 *d_sum, const uint4 *__restr
     if (tid < 2 * kNormMaxThreads / 32) s_red[0][tid] = 0.0f;
     __syncthreads();
     pdl_wait();
+    if ((int)blockIdx.x >= row_blocks) {
+        dw_columns(dy, sum, rstd_in, (int)T, nv, (int)blockIdx.x - row_blocks, reinterpret_cast<float (*)[64]>(s_rows),
+                   dw_direct);
+        return;
+    }
     auto slot = [&](int st, int tensor, int i) -> uint4 * { return s_rows + ((st * 3 + tensor) * V + i) * NT + tid; };
     auto fetch = [&](int64_t row, int st) {
         if (row < T) {
@@ -218,7 +261,7 @@ add_rmsnorm_bwd_kernel(const uint4 *dy, const uint4 *d_sum, const uint4 *__restr
         }
         cp_async_commit();   // (an empty group past the last row keeps the count)
     };
-    const int64_t step = gridDim.x;
+    const int64_t step = row_blocks;
     int64_t row = blockIdx.x;
 #pragma unroll
     for (int p = 0; p < S - 1; ++p) fetch(row + p * step, p);
@@ -431,16 +474,20 @@ extern "C" moe_status_t moe_add_rmsnorm_bwd(const moe_bf16_t *dy, const moe_bf16
     const int blocks = bwd_blocks(T, H);
     float *part = dweight ? static_cast<float *>(ws) : nullptr;
     auto u4 = [](const void *p) { return static_cast<const uint4 *>(p); };
-#define MOE_NORM_BWD(V, S)                                                                                          \
-    norm_bwd<V, S>(blocks, H, s, u4(dy), u4(d_sum), u4(sum), u4(weight), rstd, T, H, reinterpret_cast<uint4 *>(dx), \
-                   part)
+    // (not where dx overwrites dy: the column blocks read dy while the row blocks write dx)
+    const bool direct = dweight && T <= kDirectRows && 4 * T <= H && dx != dy;
+    const int grid = blocks + (direct ? (H + 63) / 64 : 0);
+    if (direct) part = nullptr;
+#define MOE_NORM_BWD(V, S)                                                                                        \
+    norm_bwd<V, S>(grid, H, s, u4(dy), u4(d_sum), u4(sum), u4(weight), rstd, T, H, reinterpret_cast<uint4 *>(dx), \
+                   part, blocks, dweight)
     if (H <= 2048) st = MOE_NORM_BWD(1, 3);   // blocks per SM: bwd_blocks
     else if (H <= 4096) st = MOE_NORM_BWD(1, 2);
     else if (H <= 16384) st = MOE_NORM_BWD(4, 2);
     else st = MOE_NORM_BWD(8, 1);
 #undef MOE_NORM_BWD
     if (st != MOE_OK) return st;
-    if (dweight)
+    if (dweight && !direct)
         launch_k(rmsnorm_dw_kernel, dim3((unsigned)((H + 31) / 32)), dim3(256), 0, s, part, blocks, H, dweight);
     return launch_status();
 }

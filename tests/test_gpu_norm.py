@@ -144,7 +144,8 @@ def bwd_reference(dy, s, w, rstd, ds):
 
 
 @pytest.mark.parametrize("T,H", [(1, 8), (1, 4096), (2, 136), (33, 2048), (333, 2056), (700, 512), (1300, 4104),
-                                 (5, 8200), (3, 32768), (4096, 128)])
+                                 (5, 8200), (3, 32768), (4096, 128), (400, 1600), (401, 1608), (400, 1592), (33, 136),
+                                 (17, 72), (100, 7168), (399, 16384)])
 @pytest.mark.parametrize("with_sum", [True, False])
 def test_backward(T, H, with_sum):
     x, r, w = inputs(T, H, seed=T + 2 * H)
@@ -162,9 +163,11 @@ def test_backward(T, H, with_sum):
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)     # the same bits
     only_x, none = moe_add_rmsnorm_bwd(dy, o.sum, w, o.rstd, d_sum=ds, want_dweight=False)
     assert none is None and torch.equal(only_x, dx)
-    in_place = dy.clone()
-    moe_add_rmsnorm_bwd(in_place, o.sum, w, o.rstd, d_sum=ds, dx=in_place)
-    assert torch.equal(in_place, dx)
+    for over in ("dy", "d_sum") if with_sum else ("dy",):
+        dy2, ds2 = dy.clone(), ds.clone() if with_sum else None
+        got, dw2 = moe_add_rmsnorm_bwd(dy2, o.sum, w, o.rstd, d_sum=ds2, dx=dy2 if over == "dy" else ds2)
+        assert torch.equal(got, dx), over
+        assert (np.abs(to_f64(dw2) - rw) <= (T + 4) * 2.0 ** -24 * wmag).all(), over
 
 
 def test_backward_against_differences():
