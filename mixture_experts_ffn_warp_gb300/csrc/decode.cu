@@ -31,6 +31,7 @@
 //   bf16   1 token, 2 of 8 experts 4096 x 14336     111 us (104)   64 tokens, 8 of 128 experts 4096 x 2048  889 us (938)
 //          13 tokens, 6 of 64 experts 2048 x 1408   124 us (118)   1 token                                 30 us (15)
 //   MXFP8  1 token, 8 of 256 experts 7168 x 2048     62 us (54)    37 tokens, 6 of 64 experts 2048 x 1408   90 us (82)
+// (in a graph; back to back on a stream the cooperative launch adds 2 us of idle time a call).
 // While it streams the kernel reads at 7 TB/s and no byte twice (ncu: 765 MB of DRAM reads for
 // 765 MB of weights); what is left is the start (about 4 us to the first weight load: launch,
 // routing, lists) and the end (about 5 us: the last segments' spread, the output's join).
@@ -399,8 +400,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     // Warp 3, which has no role, sets up barriers and TMEM; the others route.  Up to kRouteAlone
     // tokens every CTA routes for itself; more are shared out, a token a CTA, and read back
     // from topk_idx / topk_w (64 tokens of 128 experts: the routing took 10 us alone, 4 us shared).
-    // Meanwhile (MXFP8): this CTA's share of x, blocks of 32 elements, a warp each, into
-    // [H / 128] blocks of 2 T16 operand rows (first terms, then second) and a scale atom.
+    // Meanwhile (MXFP8) the warps without a token take this CTA's share of x: blocks of 32 elements,
+    // a warp each, into [H / 128] blocks of 2 T16 operand rows (first terms, then second) and a
+    // scale atom (24 tokens of 5376 x 384: 25.0 us with all warps splitting x first, 23.7).
     const bool alone = a.T <= kRouteAlone;
     int late = 0;                                      // a wait for the other CTAs' routing that gave up
     if (warp == 3) {
@@ -435,10 +437,13 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
         const int rw = warp < 3 ? warp : warp - 1;
         for (int e = rw * 32 + lane; e < a.E; e += kRouteWarps * 32) s_mask[e] = 0;
         auto meanwhile = [&]() {
+            asm volatile("barrier.cta.sync 3, %0;" ::"n"(kRouteWarps * 32) : "memory");
             if constexpr (MX) {
+                // warps without a token of their own, or all of them where every warp has one
+                const int busy = alone ? (a.T < kRouteWarps ? a.T : 0) : 1, free = kRouteWarps - busy;
                 const int nb = a.H / 32;
                 const uint32_t blk_bytes = (uint32_t)a.T16 * 256 + kSfBytes;
-                for (int b = cta * kRouteWarps + rw; b < a.T * nb; b += G * kRouteWarps) {
+                for (int b = rw < busy ? a.T * nb : cta * free + rw - busy; b < a.T * nb; b += G * free) {
                     const int t = b / nb, kb = b - t * nb;
                     uint8_t code[2], sf[2];
                     two_terms(__bfloat162float(a.x[(int64_t)t * a.H + kb * 32 + lane]), code, sf);
@@ -452,8 +457,6 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
                 }
                 fence_proxy_async_global();
             }
-            asm volatile("barrier.cta.sync 3, %0;" ::"n"(kRouteWarps * 32) : "memory");
-            if (MX && threadIdx.x == 0) count_release(&ctr->x_ready, 1);
         };
         uint32_t *mask32 = reinterpret_cast<uint32_t *>(s_mask);
         const int t0 = alone ? rw : rw == 0 ? cta : a.T, step = alone ? kRouteWarps : G;
@@ -488,6 +491,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     __syncthreads();
     sm100::tc_fence_after();
     if (late) s_abort = 1;
+    if (MX && threadIdx.x == 0) count_release(&ctr->x_ready, 1);
     // The experts that are hit, ascending, with the routes and the 16-row blocks of h before each:
     // 32 experts a warp, their totals first.  (Routes and padded rows are summed in one word:
     // 64 tokens * 32 experts keep each half below 2^16 within a chunk.)
