@@ -351,7 +351,9 @@ class MoeDecode:
     """The layer for a few tokens (token generation): routing, expert FFN and combine for up to
     T <= DECODE_MAX_TOKENS tokens a call, buffers and workspace allocated once.  router /
     expert_bias / normalize / swiglu_clamp as for MoeForward.  A call takes any number of
-    tokens up to T and returns out (bf16); topk_idx and topk_w are that call's routing."""
+    tokens up to T and returns out (bf16); topk_idx and topk_w are that call's routing.  All three
+    are the layer's own buffers: the next call overwrites them.  One call at a time: layers that
+    run on several streams at once each need their own."""
 
     def __init__(self, T: int, H: int, F: int, E: int, k: int, device="cuda", router: str = "softmax",
                  expert_bias=None, normalize: bool = True, swiglu_clamp=None):
